@@ -81,7 +81,11 @@ typedef enum {
   DSA_OP_SPARSE_MLA = 2,
   DSA_OP_FORWARD = 3,
   DSA_OP_CACHE_WRITE = 4,
-  DSA_OP_INDEXER_TOPK = 5
+  DSA_OP_INDEXER_TOPK = 5,
+  DSA_OP_DENSE_MLA = 6,
+  DSA_OP_PREFIX_MLA = 7,
+  DSA_OP_EXPANDED_MLA = 8,
+  DSA_OP_PAGE_TABLES = 9
 } dsa_op_t;
 
 /* Host struct describing a ragged batch; the arrays are DEVICE memory.
@@ -267,6 +271,68 @@ DSA_API dsa_status_t dsa_forward(const dsa_batch_t* batch, const void* q_fp8, co
 DSA_API dsa_status_t dsa_sparse_mla_no_alloc(const dsa_batch_t* batch, const void* q, int32_t n_heads,
                                              const void* kv, const int32_t* idx, int32_t k_sel, float sm_scale,
                                              void* out, float* lse, dsa_stream_t stream);
+
+/* Dense latent attention, absorbed form: dsa_sparse_mla over every position a
+ * token may see instead of a selection (contexts up to k, dense layers, the
+ * dense warm-up of the indexer).
+ *   q    [total_q, n_heads, 576] bf16     kv [total_keys, 576] bf16 latent cache
+ *   out  [total_q, n_heads, 512] bf16     lse [total_q, n_heads] fp32 or NULL
+ *   1 <= n_heads <= 128; ws of dsa_workspace_size(DSA_OP_DENSE_MLA, batch, 0,
+ *   n_heads) bytes (k_sel is not read).  Two launches; sequences of any mix of
+ *   lengths and of 0 or more query tokens each.
+ * Arithmetic: bf16 products accumulated in fp32 on the tensor cores, softmax
+ * in fp32, probabilities rounded to bf16 for the second product (relative
+ * 2^-8 each at most), one rounding to bf16 at the end.
+ * What no row sees does not reach the result, whatever it holds: cache rows behind a
+ * sequence's kv_len may be NaN.  Rows of q behind cu_q[num_seqs] (a batch
+ * padded to a captured token count) are left as they were in out and lse.
+ * A sequence whose descriptors address rows outside the cache (q_len > kv_len,
+ * kv_len > max_kv_len, kv_start + kv_len > total_keys) records
+ * DSA_ERR_DEVICE_BOUNDS and gets out = 0, lse = -inf; a page id outside the
+ * pool records it and its positions are skipped; a cu_q that does not
+ * rise from 0 within total_q records it and leaves the rows concerned unspecified. */
+DSA_API dsa_status_t dsa_dense_mla(const dsa_batch_t* batch, const void* q, int32_t n_heads, const void* kv,
+                                   float sm_scale, void* out, float* lse, void* ws, size_t ws_bytes,
+                                   dsa_stream_t stream);
+
+/* The same for a paged batch whose sequences share their first prefix_len
+ * positions (a system prompt, samples of one prompt): positions 0 ..
+ * prefix_len - 1 are read through block-table row 0 once for all rows of the
+ * batch, whose heads fill whole tiles there; positions from prefix_len on through
+ * each sequence's own row.  The result is dsa_dense_mla's of the same batch, up
+ * to rounding, where the table rows name equal entries for the prefix.
+ *   0 <= prefix_len <= max_kv_len; a sequence with kv_len - q_len < prefix_len
+ *   records DSA_ERR_DEVICE_BOUNDS and gets out = 0, lse = -inf.  Flat caches (block_table
+ *   == NULL) are DSA_ERR_UNSUPPORTED.  ws of DSA_OP_PREFIX_MLA bytes. */
+DSA_API dsa_status_t dsa_prefix_mla(const dsa_batch_t* batch, int32_t prefix_len, const void* q, int32_t n_heads,
+                                    const void* kv, float sm_scale, void* out, float* lse, void* ws, size_t ws_bytes,
+                                    dsa_stream_t stream);
+
+/* The arrays of a paged batch from the requests' lengths, on the device: each
+ * of num_seqs sequences has kv_before[b] positions and takes q_len[b] new
+ * tokens.  Pages are page_size rows (a positive multiple of 64); a sequence
+ * holds ceil(kv_before / page_size) pages in its block-table row already and
+ * takes what it lacks from free_pages, in order, sequence by sequence.
+ *   q_len, kv_before  [num_seqs] int32        free_pages [n_free] int32 page ids
+ *   block_table [num_seqs, blocks_per_seq] int32, in and out: new pages written
+ *               behind the held ones, other entries left as they were
+ *   cu_q        [num_seqs + 1] int32 out      kv_len [num_seqs] int32 out (with the new tokens)
+ *   pos         [max_tokens] int32 out: position of each new token (dsa_indexer_prep's pos)
+ *   slots       [max_tokens] int64 out: its pool row
+ *   pages_used  [1] int32 out: entries taken from free_pages
+ * Rows from the batch's last token to max_tokens (padding of a captured step)
+ * get pos = 0, slot = -1.  Outputs may not overlap the inputs or each other.
+ * DSA_ERR_DEVICE_BOUNDS is recorded, and nothing written outside the arrays, for:
+ * a negative length or one that needs more than blocks_per_seq pages (the
+ * sequence takes no tokens); too few free pages or a negative page id (entry
+ * and slots -1); more than max_tokens tokens (cu_q ends at max_tokens).
+ * ws: at least 256 bytes (device error word).  pos and slots may be NULL when
+ * max_tokens is 0, free_pages when n_free is 0. */
+DSA_API dsa_status_t dsa_page_tables(int32_t num_seqs, const int32_t* q_len, const int32_t* kv_before,
+                                     const int32_t* free_pages, int32_t n_free, int32_t page_size,
+                                     int32_t* block_table, int32_t blocks_per_seq, int32_t max_tokens, int32_t* cu_q,
+                                     int32_t* kv_len, int32_t* pos, int64_t* slots, int32_t* pages_used, void* ws,
+                                     size_t ws_bytes, dsa_stream_t stream);
 
 /* Upstream preparation ("详解DSA", the indexer code: q and k pass through a
  * per-block activation quantiser with block = the indexer head dim, one fp32

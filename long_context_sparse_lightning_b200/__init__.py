@@ -23,6 +23,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libdsa.so")
 
 OP_INDEXER, OP_TOPK, OP_SPARSE_MLA, OP_FORWARD, OP_CACHE_WRITE, OP_INDEXER_TOPK = 0, 1, 2, 3, 4, 5
+OP_DENSE_MLA, OP_PREFIX_MLA, OP_EXPANDED_MLA, OP_PAGE_TABLES = 6, 7, 8, 9
 INDEX_HEADS, INDEX_DIM, LATENT_DIM, VALUE_DIM, MAX_K_SEL = 64, 128, 576, 512, 2048
 
 STATUS = {
@@ -53,6 +54,9 @@ EXPORTS = [
     "dsa_quantize_fp8",
     "dsa_indexer_prep",
     "dsa_cache_write",
+    "dsa_dense_mla",
+    "dsa_prefix_mla",
+    "dsa_page_tables",
 ]
 
 
@@ -123,6 +127,12 @@ def _lib():
         lib.dsa_indexer_prep.restype = ctypes.c_int
         lib.dsa_cache_write.argtypes = [BP, P, P, P, P, P, P, SZ, P]
         lib.dsa_cache_write.restype = ctypes.c_int
+        lib.dsa_dense_mla.argtypes = [BP, P, I32, P, F, P, P, P, SZ, P]
+        lib.dsa_dense_mla.restype = ctypes.c_int
+        lib.dsa_prefix_mla.argtypes = [BP, I32, P, I32, P, F, P, P, P, SZ, P]
+        lib.dsa_prefix_mla.restype = ctypes.c_int
+        lib.dsa_page_tables.argtypes = [I32, P, P, P, I32, I32, P, I32, I32, P, P, P, P, P, P, SZ, P]
+        lib.dsa_page_tables.restype = ctypes.c_int
         _LIB = lib
     return _LIB
 
@@ -260,6 +270,57 @@ def forward(batch: Batch, q_fp8, q_scale, w, k_fp8, k_scale, k_sel: int, q, kv, 
     _check(_lib().dsa_forward(batch.ref, _ptr(q_fp8), _ptr(q_scale), _ptr(w), _ptr(k_fp8), _ptr(k_scale), k_sel,
                               _ptr(q), n_heads, _ptr(kv), float(sm_scale), _ptr(idx), _ptr(out), _ptr(lse), _ptr(ws),
                               ws.numel(), _stream(stream)), "dsa_forward")
+
+
+def _check_mla(where, batch, q, q_dim, out, out_dim, lse):
+    n_heads = q.shape[1] if q.dim() == 3 else 0
+    if q.dtype != torch.bfloat16 or tuple(q.shape) != (batch.total_q, n_heads, q_dim) or out.dtype != torch.bfloat16 \
+            or tuple(out.shape) != (batch.total_q, n_heads, out_dim) \
+            or (lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (batch.total_q, n_heads))):
+        raise ValueError(f"{where}: q bf16 [total_q, heads, {q_dim}], out bf16 [total_q, heads, {out_dim}], "
+                         "lse fp32 [total_q, heads] or None")
+    return int(n_heads)
+
+
+def _check_cache(where, batch, kv):
+    if kv.dtype != torch.bfloat16 or kv.dim() != 2 or kv.shape[1] != LATENT_DIM or kv.shape[0] < batch.c.total_keys:
+        raise ValueError(f"{where}: kv bf16 [total_keys, {LATENT_DIM}]")
+
+
+def dense_mla(batch: Batch, q, kv, sm_scale: float, out, lse, ws, stream=None):
+    """Latent attention over every position a token may see (absorbed form): q [total_q, heads, 576],
+    kv [total_keys, 576] -> out [total_q, heads, 512], lse (natural log) or None; ws of OP_DENSE_MLA."""
+    n_heads = _check_mla("dense_mla", batch, q, LATENT_DIM, out, VALUE_DIM, lse)
+    _check_cache("dense_mla", batch, kv)
+    _check(_lib().dsa_dense_mla(batch.ref, _ptr(q), n_heads, _ptr(kv), float(sm_scale), _ptr(out), _ptr(lse),
+                                _ptr(ws), ws.numel(), _stream(stream)), "dsa_dense_mla")
+
+
+def prefix_mla(batch: Batch, prefix_len: int, q, kv, sm_scale: float, out, lse, ws, stream=None):
+    """dense_mla of a paged batch whose sequences share their first prefix_len positions (those of block-table
+    row 0), which are read and multiplied once for all; ws of OP_PREFIX_MLA."""
+    n_heads = _check_mla("prefix_mla", batch, q, LATENT_DIM, out, VALUE_DIM, lse)
+    _check_cache("prefix_mla", batch, kv)
+    _check(_lib().dsa_prefix_mla(batch.ref, int(prefix_len), _ptr(q), n_heads, _ptr(kv), float(sm_scale), _ptr(out),
+                                 _ptr(lse), _ptr(ws), ws.numel(), _stream(stream)), "dsa_prefix_mla")
+
+
+def page_tables(q_len, kv_before, free_pages, page_size: int, block_table, cu_q, kv_len, pos, slots, pages_used, ws,
+                stream=None):
+    """Block tables, offsets, positions and cache slots of a step's new tokens from the requests' lengths:
+    q_len, kv_before int32 [B], free_pages int32 -> block_table int32 [B, blocks] (new pages written behind the
+    held ones), cu_q int32 [B + 1], kv_len int32 [B], pos int32 and slots int64 [max_tokens], pages_used int32 [1]."""
+    n, i32 = q_len.numel(), torch.int32
+    if any(t.dtype != i32 for t in (q_len, kv_before, free_pages, block_table, cu_q, kv_len, pos, pages_used)) \
+            or slots.dtype != torch.int64 or kv_before.numel() != n or block_table.dim() != 2 \
+            or block_table.shape[0] != n or cu_q.numel() != n + 1 or kv_len.numel() != n \
+            or slots.numel() != pos.numel() or pages_used.numel() != 1:
+        raise ValueError("page_tables: int32 q_len, kv_before, kv_len [B], cu_q [B + 1], block_table [B, blocks], "
+                         "free_pages, pos [max_tokens], pages_used [1]; int64 slots [max_tokens]")
+    _check(_lib().dsa_page_tables(n, _ptr(q_len), _ptr(kv_before), _ptr(free_pages), free_pages.numel(),
+                                  int(page_size), _ptr(block_table), int(block_table.shape[1]), pos.numel(),
+                                  _ptr(cu_q), _ptr(kv_len), _ptr(pos), _ptr(slots), _ptr(pages_used), _ptr(ws),
+                                  ws.numel(), _stream(stream)), "dsa_page_tables")
 
 
 def quantize_fp8(x, codes, scales, stream=None):

@@ -353,6 +353,18 @@ long long wait_budget() {
   return kDefaultBudget;
 }
 
+bool make_tmap_bf16(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint64_t ld, uint32_t box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) return false;
+  const cuuint64_t dims[2] = {cols, rows};
+  const cuuint64_t strides[1] = {ld * 2};
+  const cuuint32_t box[2] = {64, box_rows};
+  const cuuint32_t estr[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool make_mla_maps(MlaMaps* m, const void* q, int64_t total_q, int n_heads) {
   const uint64_t rows = static_cast<uint64_t>(total_q) * static_cast<uint64_t>(n_heads);
   const uint32_t h = static_cast<uint32_t>(n_heads);
@@ -377,7 +389,14 @@ size_t dsa_workspace_size(dsa_op_t op, const dsa_batch_t* batch, int32_t k_sel, 
       if (k_sel < 1 || k_sel > DSA_MAX_K_SEL || n_heads < 1 || n_heads > 128) return 0;
       return kHeaderBytes + mla_ws_bytes(batch, k_sel);
     case DSA_OP_CACHE_WRITE:
+    case DSA_OP_PAGE_TABLES:
       return kHeaderBytes;
+    case DSA_OP_DENSE_MLA:
+      return dsa::dense_ws_bytes(batch, n_heads, false);
+    case DSA_OP_PREFIX_MLA:
+      return dsa::dense_ws_bytes(batch, n_heads, true);
+    case DSA_OP_EXPANDED_MLA:
+      return n_heads < 1 || n_heads > 128 ? 0 : kHeaderBytes;
     case DSA_OP_INDEXER_TOPK:
       if (k_sel < 1 || k_sel > DSA_MAX_K_SEL) return 0;
       if (fused_cluster(batch) > 0) return kHeaderBytes;

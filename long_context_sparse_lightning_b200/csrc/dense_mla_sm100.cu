@@ -1,0 +1,936 @@
+// Dense latent attention in the absorbed form on sm_100a, and the same for a
+// batch that shares a prefix.
+//
+//     o[h] = sum_{s <= t} softmax_s(sm_scale * q[h] . c[s]) * c[s][0:512]
+//
+// over the 576-d latent rows c of every position up to the token's own (MQA
+// mode: all heads of a token attend the same rows).
+//
+// Both products are computed transposed.  A work item is up to N = 16, 32 or 64
+// query rows (heads of one token, or of a few tokens of one sequence) and a
+// range of 64-key tiles; per tile
+//     S^T [64 keys x N]  = C [64 x 576] . Q^T        (M = 64,  K = 576)
+//     O^T [512 x N]     += C[:, 0:512]^T . P^T        (4 x M = 128, K = 64)
+// so that the cache tile, as it lands by TMA, is the M-side operand of both
+// (K-major, then MN-major) and the few query rows are the N side.  With the rows
+// on the M side a 16-head rank would pay for 128 rows of tensor work, and 128
+// rows x 512 fp32 output dims would fill tensor memory and leave no room for the
+// scores; transposed, an item of 64 rows keeps 256 columns of O^T and two score
+// buffers in one CTA.
+//
+// A CTA reads 72 KB per tile.  At the measured copy bandwidth an SM gets that
+// in ~3100 cycles; the tensor work of a tile is ~1900 (N = 64) and less for
+// fewer rows, so decode is bound by the cache read.
+//
+// Work split: the (sequence, row tiles) items of a launch are laid end to end
+// by their tile counts (plus a constant for an item's prologue and epilogue), and
+// every group of W CTAs takes an equal share of that line; the W CTAs of a group
+// take neighbouring row tiles over the same keys, so that the rows a second CTA
+// needs are in L2.  An item cut by a share's border leaves normalised partial
+// outputs and log-sum-exps, at most two per CTA, which dense_merge_kernel joins.
+// Lengths are read on the device: uneven batches balance without host knowledge.
+//
+// Roles: warp 0 walks the items and issues TMA; warp 1 issues the MMAs; warps
+// 2-5 do softmax and epilogue.  Scores are read with the .16x256b shape (a thread holds
+// 2 keys x N/4 rows), so row maxima are needed across lanes: instead of a
+// running maximum per tile, a reference per row is taken from the first tile that
+// shows the row a key and kept while no score exceeds it by 2^24 (fp32 sums and
+// bf16 probabilities keep their relative precision over that range); one
+// barrier with an OR per tile decides.  Probabilities are rounded to bf16 for the
+// second product, whose other operand is the bf16 cache tile itself; row sums
+// are taken in fp32 before that rounding.
+#include <cuda_bf16.h>
+
+#include "kernels.cuh"
+#include "ptx.cuh"
+
+namespace dsa {
+namespace {
+
+constexpr int kKeys = 64;                 // keys per tile
+constexpr int kBlk = kKeys * 128;         // one [64 keys x 64 dims] block, 128-byte swizzle
+constexpr int kPair = 2 * kBlk;           // 128 value dims: one M block of the second product
+constexpr int kWarps = 6;
+constexpr int kThreads = kWarps * 32;
+constexpr int kSoftThreads = 128;
+constexpr float kGrow = 24.f;             // log2 units a score may exceed its row's reference by
+constexpr int kItemCost = 2;              // an item's prologue and epilogue, in tiles
+constexpr int kMinShare = 2;              // tiles (and item costs) a group takes at least
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t TM_S = 256;            // two score buffers of 64 columns; O^T block m at column m * N
+constexpr float kLn2 = 0.69314718055994531f;
+
+template <int N>
+struct Cfg {
+  // Scores run one tile ahead of the second product, which holds its tile's four
+  // pairs until it is done: eight pair slots at least.
+  static constexpr int ROPE_SLOTS = N == 64 ? 1 : 2;
+  static constexpr int PAIR_SLOTS = N == 64 ? 8 : (N == 32 ? 9 : 10);
+  static_assert(PAIR_SLOTS >= 8, "two tiles in flight");
+  static constexpr int OFF_Q = 0;                                    // 9 blocks of [N rows x 64 dims]
+  static constexpr int OFF_P = 9 * N * 128;                          // 2 x [64 keys x 64 rows] bf16
+  static constexpr int OFF_ROPE = OFF_P + 2 * kBlk;
+  static constexpr int OFF_PAIR = OFF_ROPE + ROPE_SLOTS * kBlk;
+  static constexpr int OFF_AUX = OFF_PAIR + PAIR_SLOTS * kPair;
+  static constexpr int SMEM = OFF_AUX + 2048 + 1024;
+  static_assert(SMEM <= 232448, "shared memory of one CTA");
+  static_assert(OFF_P % 1024 == 0, "swizzle atoms");
+};
+
+struct Item {
+  int32_t n_tiles;      // -1: no more items
+  int32_t tile0;        // first tile (position / 64)
+  int32_t row0;         // first row of the item in [total_q * H]
+  int32_t rows;         // rows of the item (<= N)
+  int32_t seq_row0;     // first row of the item's sequence
+  int32_t base;         // position of the sequence's first query
+  int32_t lo;           // first position of the item (suffix of a shared prefix)
+  int32_t last;         // last position any row of the item sees
+  int32_t slot;         // partial slot, -1: the item is whole
+  int32_t pieces;       // pieces of the item (set where begins), 0: a sequence that is out of range
+  int32_t begins;
+  int32_t prefix;       // an item of the shared prefix
+};
+
+struct Aux {
+  uint64_t q_full, q_free;
+  uint64_t rope_full[2], rope_empty[2];
+  uint64_t pair_full[10], pair_empty[10];
+  uint64_t s_full[2], s_empty[2];
+  uint64_t p_full[2], p_empty[2];
+  uint64_t o_full, o_empty;
+  uint64_t item_full[2], item_free[2];
+  Item item[2];
+  int32_t skip[10];         // the tile whose first pair has this slot lies on a page outside the pool
+  uint32_t tmem;
+  long long found_start;
+  int32_t found_seq;
+  union {
+    long long scan[8];      // block-wide reductions of the prologue
+    float mx[4][64];        // per softmax warp: row maxima / row sums
+  };
+  float fac[64];            // rescaling factors, inverse row sums
+  int32_t lim[64];          // last position each row sees
+};
+static_assert(sizeof(Aux) <= 2048, "");
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// D (TMEM) += A (shared) x B (shared), 16-bit operands.
+__device__ __forceinline__ void umma_f16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// 16 TMEM lanes x N columns, the layout of tmem_ld_16x256b_x8
+__device__ __forceinline__ void ld_scores(uint32_t t, uint32_t (&r)[32]) { tmem_ld_16x256b_x8(t, r); }
+__device__ __forceinline__ void ld_scores(uint32_t t, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+      "[%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(t));
+}
+__device__ __forceinline__ void ld_scores(uint32_t t, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(t));
+}
+// 32 lanes x 16 consecutive columns
+__device__ __forceinline__ void ld_cols16(uint32_t t, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+      "[%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(t));
+}
+
+// The softmax warps' barrier; returns the OR of `v` over them.
+__device__ __forceinline__ bool soft_any(bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, 1, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(v ? 1u : 0u)
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ void soft_sync() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
+
+// Non-finite bf16 values become 0 (both halves of a word).
+__device__ __forceinline__ uint32_t finite_or_zero(uint32_t w) {
+  if ((w & 0x7F80u) == 0x7F80u) w &= 0xFFFF0000u;
+  if ((w & 0x7F800000u) == 0x7F800000u) w &= 0x0000FFFFu;
+  return w;
+}
+
+// Entry v of the launch's work list.  With a shared prefix entry 0 is the prefix
+// (every row of the batch, positions 0 .. prefix-1) and entry v > 0 the rest
+// of sequence v - 1; without one entry v is sequence v.
+struct Entry {
+  int row0, rows;      // rows in [total_q * H]
+  int q_len, kv;
+  int b;               // sequence (block-table row; the prefix's positions go through sequence 0's)
+  int lo;              // first position
+  int gangs;           // groups of W row tiles
+  int status;          // 0, or the error site
+  bool prefix;
+};
+
+template <int N>
+__device__ __forceinline__ Entry entry_at(const DenseMlaParams& p, int v) {
+  Entry e;
+  e.status = 0;
+  e.prefix = p.shared && v == 0;
+  const int b = p.shared ? v - 1 : v;
+  if (e.prefix) {
+    const int n = min(max(__ldg(&p.cu_q[p.num_seqs]), 0), p.total_q);
+    e.row0 = 0;
+    e.rows = p.prefix_len > 0 ? n * p.n_heads : 0;
+    e.q_len = n;
+    e.kv = p.prefix_len;
+    e.b = 0;
+    e.lo = 0;
+  } else {
+    const int q0 = __ldg(&p.cu_q[b]), q1 = __ldg(&p.cu_q[b + 1]);
+    e.b = b;
+    e.kv = __ldg(&p.kv_len[b]);
+    e.lo = p.shared ? p.prefix_len : 0;
+    if (q0 < 0 || q1 < q0 || q1 > p.total_q || (b == 0 && q0 != 0)) {   // no rows of q: nothing is read or written
+      e.row0 = e.rows = e.q_len = 0;
+      e.status = 501;
+    } else {
+      e.row0 = q0 * p.n_heads;
+      e.q_len = q1 - q0;
+      e.rows = e.q_len * p.n_heads;
+      const int64_t ks = seq_start(p.pt, p.kv_start, b);
+      if (e.q_len > e.kv || e.kv > p.max_kv_len || !seq_rows_ok(p.pt, ks, e.kv, p.total_keys))
+        e.status = 502;
+      else if (e.q_len > 0 && e.kv - e.q_len < e.lo)
+        e.status = 503;                             // the sequence does not hold the whole prefix
+    }
+  }
+  e.gangs = (e.rows + N * p.gang - 1) / (N * p.gang);
+  return e;
+}
+
+// Last position the rows [.., row_end) of the entry see.
+__device__ __forceinline__ int last_seen(const DenseMlaParams& p, const Entry& e, int row_end) {
+  if (e.prefix) return e.kv - 1;
+  return e.kv - e.q_len + (row_end - 1) / p.n_heads;
+}
+
+// Tiles of gang g of the entry (0 for an entry that is out of range).
+template <int N>
+__device__ __forceinline__ int gang_tiles(const DenseMlaParams& p, const Entry& e, int g) {
+  if (e.status != 0) return 0;
+  const int end = min(e.rows, (g + 1) * N * p.gang);
+  return last_seen(p, e, end) / kKeys + 1 - e.lo / kKeys;
+}
+
+template <int N>
+__device__ __forceinline__ long long entry_cost(const DenseMlaParams& p, int v) {
+  const Entry e = entry_at<N>(p, v);
+  if (e.prefix || e.gangs <= 1 || e.status != 0)
+    return e.gangs > 0 ? static_cast<long long>(e.gangs) * (gang_tiles<N>(p, e, 0) + kItemCost) : 0;
+  long long c = 0;
+  for (int g = 0; g < e.gangs; ++g) c += gang_tiles<N>(p, e, g) + kItemCost;
+  return c;
+}
+
+template <int N>
+__global__ void __launch_bounds__(kThreads, 1)
+    dense_mla_kernel(const DenseMlaParams p, const __grid_constant__ CUtensorMap map_q,
+                     const __grid_constant__ CUtensorMap map_c) {
+  using C = Cfg<N>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  uint8_t* sm = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+  Aux* ax = reinterpret_cast<Aux*>(sm + C::OFF_AUX);
+  const uint32_t warp = warp_id(), lane = lane_id();
+  const int tid = threadIdx.x;
+  const int H = p.n_heads;
+
+  if (tid == 0) {
+    mbar_init(&ax->q_full, 1);
+    mbar_init(&ax->q_free, 1);
+    for (int i = 0; i < C::ROPE_SLOTS; ++i) {
+      mbar_init(&ax->rope_full[i], 1);
+      mbar_init(&ax->rope_empty[i], 1);
+    }
+    for (int i = 0; i < C::PAIR_SLOTS; ++i) {
+      mbar_init(&ax->pair_full[i], 1);
+      mbar_init(&ax->pair_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ax->s_full[i], 1);
+      mbar_init(&ax->s_empty[i], 4);
+      mbar_init(&ax->p_full[i], 4);
+      mbar_init(&ax->p_empty[i], 1);
+      mbar_init(&ax->item_full[i], 1);
+      mbar_init(&ax->item_free[i], 5);      // the MMA thread and the softmax warps
+    }
+    mbar_init(&ax->o_full, 1);
+    mbar_init(&ax->o_empty, 4);
+    fence_mbar_init();
+    prefetch_tmap(&map_q);
+    prefetch_tmap(&map_c);
+    ax->found_seq = -1;
+  }
+  if (warp == 1) {
+    tmem_alloc(&ax->tmem, kTmemCols);
+    tmem_relinquish();
+  }
+
+  // ---- this group's share of the work line ----
+  const int n_entries = p.num_seqs + (p.shared ? 1 : 0);
+  long long mine = 0;
+  for (int v = tid; v < n_entries; v += kThreads) mine += entry_cost<N>(p, v);
+  {
+    long long s = mine;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (lane == 0) ax->scan[warp] = s;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  long long total = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) total += ax->scan[w];
+  const int group = static_cast<int>(blockIdx.x) / p.gang, member = static_cast<int>(blockIdx.x) % p.gang;
+  const int n_groups = static_cast<int>(
+      min(static_cast<long long>(gridDim.x / p.gang), max(1LL, (total + kMinShare - 1) / kMinShare)));
+  const long long lo = group < n_groups ? total * group / n_groups : total;
+  const long long hi = group < n_groups ? total * (group + 1) / n_groups : total;
+  __syncthreads();
+  // the entry that holds position lo of the line
+  if (lo < hi) {
+    long long base = 0;
+    for (int v0 = 0; v0 < n_entries; v0 += kThreads) {
+      const int v = v0 + tid;
+      const long long c = v < n_entries ? entry_cost<N>(p, v) : 0;
+      long long inc = c;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long t = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= static_cast<uint32_t>(o)) inc += t;
+      }
+      if (lane == 31) ax->scan[warp] = inc;
+      __syncthreads();
+      long long before = base, all = 0;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        if (w < static_cast<int>(warp)) before += ax->scan[w];
+        all += ax->scan[w];
+      }
+      const long long start = before + inc - c;
+      if (c > 0 && start <= lo && lo < start + c) {
+        ax->found_seq = v;
+        ax->found_start = start;
+      }
+      base += all;
+      __syncthreads();
+      if (base > lo) break;      // uniform
+    }
+  }
+  const uint32_t tmem = ax->tmem;
+
+  if (warp == 0) {
+    // --------------------------------------------------- items and TMA loads --
+    bool ok = true;
+    auto wait = [&](uint64_t* b, uint32_t parity, uint32_t site) {
+      if (ok && !mbar_wait(b, parity, p.budget)) {
+        if (lane == 0) report_error(p.err, kDevErrTimeout, site, blockIdx.x);
+        ok = false;
+      }
+      ok = __all_sync(0xffffffffu, ok);
+    };
+    if (blockIdx.x == 0)      // sequences that are out of range, once per launch
+      for (int v = static_cast<int>(lane); v < n_entries; v += 32) {
+        const Entry e = entry_at<N>(p, v);
+        if (e.status != 0) report_error(p.err, kDevErrBounds, e.status, e.b);
+      }
+    int k = 0, n_q = 0, n_rope = 0, n_pair = 0;
+    auto publish = [&](const Item& it) {
+      if (k >= 2) wait(&ax->item_free[k & 1], ((k >> 1) + 1) & 1, 510);
+      if (ok && lane == 0) {
+        ax->item[k & 1] = it;
+        mbar_arrive(&ax->item_full[k & 1]);
+      }
+      __syncwarp();
+      ++k;
+    };
+    int v = lo < hi ? ax->found_seq : -1;
+    long long at = lo;                                       // position on the line
+    long long start = v >= 0 ? ax->found_start : 0;          // of gang g of entry v
+    Entry e;
+    int g = 0;
+    if (v >= 0) e = entry_at<N>(p, v);
+    while (ok && v >= 0 && at < hi) {
+      const int nt = gang_tiles<N>(p, e, g);
+      const long long next = start + nt + kItemCost;
+      if (at >= next) {                                      // this share begins behind gang g
+        start = next;
+        if (++g >= e.gangs) {
+          g = 0;
+          do ++v;
+          while (v < n_entries && (e = entry_at<N>(p, v)).gangs == 0);
+          if (v >= n_entries) break;
+        }
+        continue;
+      }
+      const int t0 = static_cast<int>(min(at - start, static_cast<long long>(nt)));
+      const int t1 = static_cast<int>(min(hi - start, static_cast<long long>(nt)));
+      const bool begins = at == start;
+      at = min(hi, next);
+      if (!begins && t0 == t1) continue;                     // only the item's constant cost is left
+      const int first = (g * p.gang + member) * N;           // row tile of this member
+      if (first >= e.rows) continue;
+      Item it;
+      it.rows = min(N, e.rows - first);
+      it.row0 = e.row0 + first;
+      it.seq_row0 = e.row0;
+      it.base = e.kv - e.q_len;
+      it.lo = e.lo;
+      it.prefix = e.prefix ? 1 : 0;
+      it.begins = begins ? 1 : 0;
+      it.pieces = 0;
+      it.last = -1;
+      it.tile0 = e.lo / kKeys + t0;
+      it.n_tiles = 0;
+      it.slot = -1;
+      if (e.status == 0) {
+        it.last = last_seen(p, e, first + it.rows);
+        const int own = it.last / kKeys + 1 - e.lo / kKeys;  // this row tile may end before the gang's last
+        it.n_tiles = max(0, min(t1, own) - t0);
+        const long long x = start + nt;                      // one past the item's last tile
+        const int g_last = static_cast<int>((x * n_groups - 1) / total);
+        it.pieces = begins ? g_last - group + 1 : 0;
+        if (!begins || t1 < nt) it.slot = static_cast<int>(blockIdx.x) * 2 + (begins ? 1 : 0);
+      }
+      publish(it);
+      if (!ok || it.n_tiles == 0) continue;
+      if (n_q > 0) wait(&ax->q_free, (n_q - 1) & 1, 511);
+      if (!ok) break;
+      ++n_q;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&ax->q_full, 9 * N * 128);
+        for (int c = 0; c < 9; ++c) tma_load_2d(sm + C::OFF_Q + c * N * 128, &map_q, &ax->q_full, c * 64, it.row0);
+      }
+      __syncwarp();
+      const int64_t kstart = seq_start(p.pt, p.kv_start, e.b);
+      int my_row = 0;
+      for (int i = 0; ok && i < it.n_tiles; ++i) {
+        if ((i & 31) == 0) {            // cache rows of the next 32 tiles, one per lane (a tile lies in one page)
+          const int t = min(i + static_cast<int>(lane), it.n_tiles - 1);
+          const int64_t r = cache_row(p.pt, e.b, kstart, (it.tile0 + t) * kKeys);
+          if (r < 0) report_error(p.err, kDevErrBounds, 504, e.b);
+          my_row = r < 0 ? -1 : static_cast<int>(r);
+        }
+        int row = __shfl_sync(0xffffffffu, my_row, i & 31);
+        const int skip = row < 0 ? 1 : 0;
+        if (skip) row = static_cast<int>(p.total_keys);      // past the pool: zeros arrive, no row is read
+        const int rs = n_rope % C::ROPE_SLOTS;
+        if (n_rope >= C::ROPE_SLOTS) wait(&ax->rope_empty[rs], ((n_rope / C::ROPE_SLOTS) + 1) & 1, 512);
+        if (!ok) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&ax->rope_full[rs], kBlk);
+          tma_load_2d(sm + C::OFF_ROPE + rs * kBlk, &map_c, &ax->rope_full[rs], 512, row);
+        }
+        ++n_rope;
+        for (int m = 0; ok && m < 4; ++m) {
+          const int ps = n_pair % C::PAIR_SLOTS;
+          if (n_pair >= C::PAIR_SLOTS) wait(&ax->pair_empty[ps], ((n_pair / C::PAIR_SLOTS) + 1) & 1, 513);
+          if (!ok) break;
+          if (lane == 0) {
+            uint8_t* dst = sm + C::OFF_PAIR + ps * kPair;
+            if (m == 0) ax->skip[ps] = skip;
+            mbar_arrive_expect_tx(&ax->pair_full[ps], kPair);
+            tma_load_2d(dst, &map_c, &ax->pair_full[ps], m * 128, row);
+            tma_load_2d(dst + kBlk, &map_c, &ax->pair_full[ps], m * 128 + 64, row);
+          }
+          ++n_pair;
+        }
+      }
+    }
+    if (ok) {
+      Item end;
+      end.n_tiles = -1;
+      publish(end);
+    }
+    if (!ok) {
+      // a wait ran out: let the copies in flight land before the block ends
+      bool landed = true;
+      if (n_q > 0) landed = mbar_wait(&ax->q_full, (n_q - 1) & 1, p.budget) && landed;
+      for (int i = max(0, n_rope - C::ROPE_SLOTS); landed && i < n_rope; ++i)
+        landed = mbar_wait(&ax->rope_full[i % C::ROPE_SLOTS], (i / C::ROPE_SLOTS) & 1, p.budget);
+      for (int i = max(0, n_pair - C::PAIR_SLOTS); landed && i < n_pair; ++i)
+        landed = mbar_wait(&ax->pair_full[i % C::PAIR_SLOTS], (i / C::PAIR_SLOTS) & 1, p.budget);
+    }
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- MMAs --
+    if (elect_one()) {
+      constexpr uint32_t idesc_s = idesc_f32acc(kFmtBF16, kFmtBF16, 64, N, 0, 0);    // C and Q K-major
+      constexpr uint32_t idesc_o = idesc_f32acc(kFmtBF16, kFmtBF16, 128, N, 1, 1);   // C^T and P^T MN-major
+      const uint32_t q_addr = smem_u32(sm + C::OFF_Q), p_addr = smem_u32(sm + C::OFF_P);
+      const uint32_t rope_addr = smem_u32(sm + C::OFF_ROPE), pair_addr = smem_u32(sm + C::OFF_PAIR);
+      bool ok = true;
+      auto wait = [&](uint64_t* b, uint32_t parity, uint32_t site) {
+        if (ok && !mbar_wait(b, parity, p.budget)) {
+          report_error(p.err, kDevErrTimeout, site, blockIdx.x);
+          ok = false;
+        }
+        return ok;
+      };
+      int n_q = 0, t_s = 0, t_o = 0, n_o = 0;      // Q tiles, tiles scored, tiles accumulated, items accumulated
+      auto score = [&](bool last) {
+        const int rs = t_s % C::ROPE_SLOTS, sb = t_s & 1;
+        const uint32_t d = tmem + TM_S + sb * 64;
+        if (t_s >= 2 && !wait(&ax->s_empty[sb], ((t_s >> 1) + 1) & 1, 521)) return;
+        if (!wait(&ax->rope_full[rs], (t_s / C::ROPE_SLOTS) & 1, 522)) return;
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          umma_f16_ss(d, smem_desc(rope_addr + rs * kBlk + kk * 32, 16, 1024, kSwizzle128B),
+                      smem_desc(q_addr + 8 * N * 128 + kk * 32, 16, 1024, kSwizzle128B), idesc_s, kk ? 1u : 0u);
+        umma_commit(&ax->rope_empty[rs]);
+        for (int m = 0; m < 4; ++m) {
+          const int n = 4 * t_s + m, ps = n % C::PAIR_SLOTS;
+          if (!wait(&ax->pair_full[ps], (n / C::PAIR_SLOTS) & 1, 523)) return;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            umma_f16_ss(d, smem_desc(pair_addr + ps * kPair + (kk >> 2) * kBlk + (kk & 3) * 32, 16, 1024, kSwizzle128B),
+                        smem_desc(q_addr + (2 * m + (kk >> 2)) * N * 128 + (kk & 3) * 32, 16, 1024, kSwizzle128B),
+                        idesc_s, 1u);
+        }
+        umma_commit(&ax->s_full[sb]);
+        if (last) umma_commit(&ax->q_free);
+        ++t_s;
+      };
+      for (int k = 0; ok; ++k) {
+        if (!wait(&ax->item_full[k & 1], (k >> 1) & 1, 520)) break;
+        const int nt = ax->item[k & 1].n_tiles;
+        mbar_arrive(&ax->item_free[k & 1]);
+        if (nt < 0) break;
+        if (nt == 0) continue;
+        if (!wait(&ax->q_full, n_q & 1, 524)) break;
+        ++n_q;
+        score(nt == 1);
+        for (int i = 0; ok && i < nt; ++i) {
+          if (i + 1 < nt) score(i + 2 == nt);
+          const int pb = t_o & 1;
+          if (!ok || !wait(&ax->p_full[pb], (t_o >> 1) & 1, 525)) break;
+          if (i == 0 && n_o > 0 && !wait(&ax->o_empty, (n_o - 1) & 1, 526)) break;
+          tc_fence_after();
+          for (int m = 0; m < 4; ++m) {
+            const int ps = (4 * t_o + m) % C::PAIR_SLOTS;
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              umma_f16_ss(tmem + m * N, smem_desc(pair_addr + ps * kPair + kk * 2048, kBlk, 1024, kSwizzle128B),
+                          smem_desc(p_addr + pb * kBlk + kk * 2048, kBlk, 1024, kSwizzle128B), idesc_o,
+                          (i | kk) ? 1u : 0u);
+            umma_commit(&ax->pair_empty[ps]);
+          }
+          umma_commit(&ax->p_empty[pb]);
+          ++t_o;
+          if (i + 1 == nt) umma_commit(&ax->o_full);
+        }
+        ++n_o;
+      }
+    }
+  } else {
+    // ---------------------------------------------------- softmax, epilogue --
+    // Warp of lane quarter qd holds keys 16 qd .. 16 qd + 15 of a tile (an M = 64
+    // accumulator occupies the first 16 lanes of each quarter).
+    constexpr int KC = N / 8;
+    const int qd = static_cast<int>(warp & 3u);
+    const uint32_t lane_base = static_cast<uint32_t>(qd * 32) << 16;
+    const int key0 = 16 * qd + static_cast<int>(lane >> 2);        // and key0 + 8
+    const int col0 = 2 * static_cast<int>(lane & 3u);              // columns 8 kc + col0 + {0, 1}
+    const int st = tid - 64;                                       // 0 .. 127
+    const float NEG_INF = __int_as_float(0xff800000);
+    const float scale = p.scale_log2;
+    const uint32_t p_base = smem_u32(sm + C::OFF_P);
+    bool ok = true;
+    // Once a wait has run out nothing waits any more: the warps go on to the
+    // end in step (their barriers keep matching) and the error word tells.
+    auto wait = [&](uint64_t* b, uint32_t parity, uint32_t site) {
+      if (ok && !mbar_wait(b, parity, p.budget)) {
+        report_error(p.err, kDevErrTimeout, site, blockIdx.x);
+        ok = false;
+      }
+      ok = __all_sync(0xffffffffu, ok);
+    };
+    int t = 0, n_o = 0;       // tiles and items so far
+    for (int k = 0;; ++k) {
+      wait(&ax->item_full[k & 1], (k >> 1) & 1, 530);
+      // a warp that gave up must not leave the others at a barrier
+      if (soft_any(!ok)) break;
+      const Item it = ax->item[k & 1];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ax->item_free[k & 1]);
+      if (it.n_tiles < 0) break;
+      if (st < N)
+        ax->lim[st] = st >= it.rows ? -1 : (it.prefix ? it.last : it.base + (it.row0 + st - it.seq_row0) / H);
+      soft_sync();
+      const int min_lim = ax->lim[0];       // row 0 is the earliest token's
+      float mr[2 * KC], l[2 * KC];
+#pragma unroll
+      for (int c = 0; c < 2 * KC; ++c) {
+        mr[c] = NEG_INF;
+        l[c] = 0.f;
+      }
+      for (int i = 0; i < it.n_tiles; ++i, ++t) {
+        const int sb = t & 1, pos0 = (it.tile0 + i) * kKeys;
+        uint32_t s[4 * KC];
+        wait(&ax->s_full[sb], (t >> 1) & 1, 531);
+        tc_fence_after();
+        ld_scores(tmem + lane_base + TM_S + sb * 64, s);
+        tmem_ld_wait();
+        tc_fence_before();
+        const int skip = ax->skip[4 * t % C::PAIR_SLOTS];   // kept until the slot is refilled, after this tile's product
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ax->s_empty[sb]);
+        const bool border = skip != 0 || pos0 < it.lo || pos0 + kKeys - 1 > min_lim;
+        if (border) {
+#pragma unroll
+          for (int kc = 0; kc < KC; ++kc)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int pos = pos0 + key0 + (e >> 1) * 8;
+              if (skip || pos < it.lo || pos > ax->lim[8 * kc + col0 + (e & 1)]) s[4 * kc + e] = __float_as_uint(NEG_INF);
+            }
+        }
+        bool grow = false;
+#pragma unroll
+        for (int kc = 0; kc < KC; ++kc)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            // reference -inf: any finite score grows it, a masked one (NaN here) does not
+            grow |= fmaf(__uint_as_float(s[4 * kc + e]), scale, -mr[2 * kc + (e & 1)]) > kGrow;
+        if (soft_any(grow)) {
+          // new references: the tile's row maxima where they exceed the old ones
+#pragma unroll
+          for (int c = 0; c < 2 * KC; ++c) {
+            float m = fmaxf(__uint_as_float(s[4 * (c >> 1) + (c & 1)]), __uint_as_float(s[4 * (c >> 1) + 2 + (c & 1)]));
+#pragma unroll
+            for (int o = 4; o <= 16; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            if (lane < 4) ax->mx[qd][8 * (c >> 1) + col0 + (c & 1)] = m;
+          }
+          soft_sync();
+#pragma unroll
+          for (int c = 0; c < 2 * KC; ++c) {
+            const int n = 8 * (c >> 1) + col0 + (c & 1);
+            const float m = fmaxf(fmaxf(ax->mx[0][n], ax->mx[1][n]), fmaxf(ax->mx[2][n], ax->mx[3][n])) * scale;
+            const float f = m > mr[c] ? exp2_approx(mr[c] - m) : 1.f;
+            mr[c] = fmaxf(mr[c], m);
+            l[c] *= f;
+            if (qd == 0 && (lane >> 2) == 0) ax->fac[n] = f;
+          }
+          soft_sync();
+          if (i > 0) {
+            // O^T is idle once the previous tile's product is done
+            wait(&ax->p_empty[(t - 1) & 1], ((t - 1) >> 1) & 1, 532);
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < 4 * N; c += 16) {
+              uint32_t o[16];
+              ld_cols16(tmem + lane_base + c, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int j = 0; j < 16; ++j)
+                o[j] = __float_as_uint(__uint_as_float(o[j]) * ax->fac[(c + j) % N]);
+              tmem_st16(tmem + lane_base + c, o);
+            }
+            tmem_st_wait();
+            tc_fence_before();
+          }
+        }
+        if (t >= 2) wait(&ax->p_empty[t & 1], ((t >> 1) + 1) & 1, 533);
+        const uint32_t pbuf = p_base + (t & 1) * kBlk;
+#pragma unroll
+        for (int kc = 0; kc < KC; ++kc) {
+          float x[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float m = mr[2 * kc + (e & 1)];
+            x[e] = exp2_approx(fmaf(__uint_as_float(s[4 * kc + e]), scale, m == NEG_INF ? 0.f : -m));
+          }
+          l[2 * kc] += x[0] + x[2];
+          l[2 * kc + 1] += x[1] + x[3];
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const int key = key0 + 8 * r;
+            asm volatile("st.shared.b32 [%0], %1;" ::"r"(pbuf + key * 128 + ((kc ^ (key & 7)) << 4) + col0 * 2),
+                         "r"(pack_bf16(x[2 * r], x[2 * r + 1]))
+                         : "memory");
+          }
+        }
+        if (border) {
+          // Keys that some row must not see: 0 x a non-finite value would reach that
+          // row, so such values become 0 in the tile.  A row that does see the key
+          // has its NaN from the score.
+#pragma unroll 1
+          for (int m = 0; m < 4; ++m) {
+            const int n = 4 * t + m, ps = n % C::PAIR_SLOTS;
+            wait(&ax->pair_full[ps], (n / C::PAIR_SLOTS) & 1, 534);
+            uint8_t* blk = sm + C::OFF_PAIR + ps * kPair;
+#pragma unroll 1
+            for (int u = st; u < kPair / 16; u += kSoftThreads) {
+              const int pos = pos0 + ((u >> 3) & 63);
+              if (pos >= it.lo && pos <= min_lim) continue;
+              uint4* w = reinterpret_cast<uint4*>(blk) + u;
+              const uint4 a = *w;
+              const uint4 b = make_uint4(finite_or_zero(a.x), finite_or_zero(a.y), finite_or_zero(a.z), finite_or_zero(a.w));
+              if (a.x != b.x || a.y != b.y || a.z != b.z || a.w != b.w) *w = b;
+            }
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ax->p_full[t & 1]);
+      }
+
+      // ---- row sums over the tile's keys: 8 lanes, then 4 warps ----
+#pragma unroll
+      for (int c = 0; c < 2 * KC; ++c) {
+        float v = l[c];
+#pragma unroll
+        for (int o = 4; o <= 16; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        if (lane < 4) ax->mx[qd][8 * (c >> 1) + col0 + (c & 1)] = v;
+      }
+      soft_sync();
+      if (qd == 0 && lane < 4) {
+#pragma unroll
+        for (int c = 0; c < 2 * KC; ++c) {
+          const int n = 8 * (c >> 1) + col0 + (c & 1);
+          const float v = (ax->mx[0][n] + ax->mx[1][n]) + (ax->mx[2][n] + ax->mx[3][n]);
+          ax->fac[n] = v == 0.f ? 0.f : 1.f / v;
+          const float lse2 = v == 0.f ? NEG_INF : mr[c] + log2f(v);      // log2 of the sum of exponentials
+          if (n < it.rows) {
+            const int r = it.row0 + n;
+            if (it.slot >= 0) {
+              p.part_lse[static_cast<int64_t>(it.slot) * N + n] = lse2;
+            } else if (p.shared) {
+              p.row_lse[static_cast<int64_t>(it.prefix ? 0 : 1) * p.total_q * H + r] = lse2;
+            } else if (p.lse != nullptr) {
+              p.lse[r] = lse2 * kLn2;
+            }
+            if (it.begins)
+              p.rec[static_cast<int64_t>(p.shared && !it.prefix ? 1 : 0) * p.total_q * H + r] =
+                  make_int4(it.slot, it.pieces, n, p.gang);
+          }
+        }
+      }
+      soft_sync();
+      if (it.n_tiles > 0) {
+        wait(&ax->o_full, n_o & 1, 535);
+        ++n_o;
+        tc_fence_after();
+      }
+      const int d0 = qd * 32 + static_cast<int>(lane);
+      float* dst32 = nullptr;
+      if (it.slot >= 0) {
+        dst32 = p.part_o + static_cast<int64_t>(it.slot) * N * 512;
+      } else if (p.shared) {
+        dst32 = p.row_o + (static_cast<int64_t>(it.prefix ? 0 : 1) * p.total_q * H + it.row0) * 512;
+      }
+#pragma unroll 1
+      for (int c = 0; c < 4 * N; c += 16) {
+        uint32_t o[16];
+        if (it.n_tiles > 0) {
+          ld_cols16(tmem + lane_base + c, o);
+          tmem_ld_wait();
+        } else {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) o[j] = 0u;
+        }
+        const int n0 = c % N, d = (c / N) * 128 + d0;
+        if (dst32 != nullptr) {
+          if (it.n_tiles > 0) {          // an empty piece has lse = -inf, its output is not read
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              if (n0 + j < it.rows)
+                dst32[static_cast<int64_t>(n0 + j) * 512 + d] = __uint_as_float(o[j]) * ax->fac[n0 + j];
+          }
+        } else {
+          // lane pairs exchange so that each stores two neighbouring dims of one row
+#pragma unroll
+          for (int j = 0; j < 16; j += 2) {
+            const float a = __uint_as_float(o[j]) * ax->fac[n0 + j], b = __uint_as_float(o[j + 1]) * ax->fac[n0 + j + 1];
+            const bool odd = (lane & 1u) != 0;
+            const float got = __shfl_xor_sync(0xffffffffu, odd ? a : b, 1);
+            const uint32_t w = odd ? pack_bf16(got, b) : pack_bf16(a, got);
+            const int n = n0 + j + (odd ? 1 : 0);
+            if (n < it.rows)
+              *reinterpret_cast<uint32_t*>(p.out + static_cast<int64_t>(it.row0 + n) * 512 + (d & ~1)) = w;
+          }
+        }
+      }
+      if (it.n_tiles > 0) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ax->o_empty);
+      }
+      soft_sync();          // fac and lim may be rewritten
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// One row's pieces: log-sum-exps and outputs of the partial slots (or the one
+// whole result), joined with weights 2^(lse_i - max).
+struct RowPieces {
+  const float* lse;
+  const float* o;
+  int64_t lse_step, o_step, lse_first, o_first;    // piece 0 at offset 0, piece i > 0 at first + (i - 1) * step
+  int n;
+};
+
+__device__ __forceinline__ RowPieces row_pieces(const DenseMlaParams& p, int rec_half, int64_t row, int N, int n_slots) {
+  const int64_t rows = static_cast<int64_t>(p.total_q) * p.n_heads;
+  const int4 r = p.rec[rec_half * rows + row];
+  RowPieces x;
+  x.lse_step = x.o_step = x.lse_first = x.o_first = 0;
+  x.n = 0;
+  if (r.x < 0) {                           // whole (shared prefix) or out of range (no pieces)
+    if (p.shared && r.y > 0) {
+      x.n = 1;
+      x.lse = p.row_lse + rec_half * rows + row;
+      x.o = p.row_o + (rec_half * rows + row) * 512;
+    }
+    return x;
+  }
+  // pieces: slot r.x, then slot 0 of every following group's member
+  const int64_t last = static_cast<int64_t>(r.x >> 1) + static_cast<int64_t>(r.y - 1) * r.w;
+  if (r.y < 1 || r.z < 0 || r.z >= N || r.w < 1 || last * 2 + 1 >= n_slots) return x;      // not a record of this launch
+  x.n = r.y;
+  x.lse = p.part_lse + static_cast<int64_t>(r.x) * N + r.z;
+  x.o = p.part_o + (static_cast<int64_t>(r.x) * N + r.z) * 512;
+  const int64_t step = 2 * static_cast<int64_t>(r.w);
+  x.lse_step = step * N;
+  x.o_step = step * N * 512;
+  x.lse_first = (step - 1) * N;            // slot 2c + 1 -> slot 2(c + W)
+  x.o_first = (step - 1) * N * 512;
+  return x;
+}
+
+// A block of 128 threads per row, four dims a thread.
+__global__ void __launch_bounds__(128) dense_merge_kernel(const DenseMlaParams p, int N, int n_slots) {
+  const float NEG_INF = __int_as_float(0xff800000);
+  const int64_t rows = static_cast<int64_t>(min(max(__ldg(&p.cu_q[p.num_seqs]), 0), p.total_q)) * p.n_heads;
+  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
+    RowPieces a = row_pieces(p, 0, row, N, n_slots), b;
+    b.n = 0;
+    bool dead = false;
+    if (p.shared) {
+      b = row_pieces(p, 1, row, N, n_slots);
+      dead = b.n == 0;                     // the row's sequence is out of range
+      if (p.prefix_len == 0) a.n = 0;
+    } else if (a.n == 0) {
+      continue;                            // the main kernel wrote the row
+    }
+    float m = NEG_INF;
+    for (int i = 0; i < a.n; ++i) m = fmaxf(m, a.lse[i == 0 ? 0 : a.lse_first + (i - 1) * a.lse_step]);
+    for (int i = 0; i < b.n; ++i) m = fmaxf(m, b.lse[i == 0 ? 0 : b.lse_first + (i - 1) * b.lse_step]);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float sum = 0.f;
+    const float ref = m == NEG_INF ? 0.f : m;
+    auto add = [&](const RowPieces& x) {
+#pragma unroll 4
+      for (int i = 0; i < x.n; ++i) {
+        const float z = x.lse[i == 0 ? 0 : x.lse_first + (i - 1) * x.lse_step];
+        if (z == NEG_INF) continue;
+        const float w = exp2f(z - ref);
+        const float4 o =
+            *reinterpret_cast<const float4*>(x.o + (i == 0 ? 0 : x.o_first + (i - 1) * x.o_step) + threadIdx.x * 4);
+        sum += w;
+        acc.x += w * o.x;
+        acc.y += w * o.y;
+        acc.z += w * o.z;
+        acc.w += w * o.w;
+      }
+    };
+    if (!dead) {
+      add(a);
+      add(b);
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    uint2 w;
+    w.x = pack_bf16(acc.x * inv, acc.y * inv);
+    w.y = pack_bf16(acc.z * inv, acc.w * inv);
+    *reinterpret_cast<uint2*>(p.out + row * 512 + threadIdx.x * 4) = w;
+    if (threadIdx.x == 0 && p.lse != nullptr) p.lse[row] = sum == 0.f ? NEG_INF : (ref + log2f(sum)) * kLn2;
+  }
+}
+
+template <int N>
+cudaError_t launch(const DenseMlaParams& p, const CUtensorMap& map_q, const CUtensorMap& map_c, int ctas,
+                   cudaStream_t stream) {
+  cudaError_t e = cudaFuncSetAttribute(dense_mla_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<N>::SMEM);
+  if (e != cudaSuccess) return e;
+  dense_mla_kernel<N><<<ctas, kThreads, Cfg<N>::SMEM, stream>>>(p, map_q, map_c);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+DensePlan dense_plan(const dsa_batch_t* b, int n_heads, bool shared) {
+  DensePlan d;
+  // Rows an item can hold: the rows of one sequence, or with a shared prefix
+  // of the whole batch.
+  const int64_t rows = static_cast<int64_t>(shared ? b->total_q : b->max_q_per_seq) * n_heads;
+  d.n = rows <= 16 ? 16 : (rows <= 32 ? 32 : 64);
+  // CTAs that share a key range: the row tiles of an average sequence, in equal
+  // gangs of at most 16.
+  const int64_t tiles = (static_cast<int64_t>(b->total_q) * n_heads + static_cast<int64_t>(b->num_seqs) * d.n - 1) /
+                        (static_cast<int64_t>(b->num_seqs) * d.n);
+  const int64_t t = tiles < 1 ? 1 : tiles, parts = (t + 15) / 16;
+  d.gang = static_cast<int>((t + parts - 1) / parts);
+  return d;
+}
+
+cudaError_t launch_dense_mla(const DenseMlaParams& p, const DensePlan& d, const CUtensorMap& map_q,
+                             const CUtensorMap& map_c, cudaStream_t stream) {
+  int sms = sm_count();
+  if (sms < 1 || sms > kDenseMaxCtas) sms = kDenseMaxCtas;
+  const int ctas = sms / d.gang * d.gang;
+  cudaError_t e;
+  switch (d.n) {
+    case 16: e = launch<16>(p, map_q, map_c, ctas, stream); break;
+    case 32: e = launch<32>(p, map_q, map_c, ctas, stream); break;
+    default: e = launch<64>(p, map_q, map_c, ctas, stream); break;
+  }
+  if (e != cudaSuccess) return e;
+  const int64_t rows = static_cast<int64_t>(p.total_q) * p.n_heads;
+  const int grid = static_cast<int>(rows < 148 * 16 ? rows : 148 * 16);
+  dense_merge_kernel<<<grid, 128, 0, stream>>>(p, d.n, 2 * kDenseMaxCtas);
+  return cudaGetLastError();
+}
+
+}  // namespace dsa

@@ -27,6 +27,9 @@ struct PageTable {
 // argument checks (DSA_OK or the status to return) and its page table.
 dsa_status_t validate_batch(const dsa_batch_t* b);
 PageTable batch_pages(const dsa_batch_t* b);
+// TMA descriptor of a row-major [rows, cols] view of 16-bit elements whose rows are
+// `ld` elements apart, box [box_rows, 64], 128-byte swizzle; false if refused.
+bool make_tmap_bf16(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint64_t ld, uint32_t box_rows);
 #ifdef __CUDACC__
 // First cache row of sequence b (flat caches; 0 when paged, where kv_start
 // may be null).
@@ -50,6 +53,9 @@ __device__ __forceinline__ int64_t cache_row(const PageTable& pt, int b, int64_t
   return static_cast<int64_t>(pg) * pt.page + s % pt.page;
 }
 #endif
+
+// Workspace bytes of the dense latent attentions (0: arguments the kernels do not take)
+size_t dense_ws_bytes(const dsa_batch_t* b, int n_heads, bool shared);
 
 // clock64 cycles one bounded device wait may take before it records
 // DSA_ERR_DEVICE_TIMEOUT: DSA_WAIT_BUDGET_CYCLES if set (> 0), else ~1 s
@@ -197,6 +203,64 @@ cudaError_t launch_sparse_mla(const MlaParams& p, const MlaMaps& maps, cudaStrea
 cudaError_t launch_sparse_mla_fp16(const MlaParams& p, const MlaMaps& maps, cudaStream_t stream);
 cudaError_t launch_latent_to_fp16(const uint16_t* src, uint16_t* dst, int64_t n_elems, cudaStream_t stream);
 cudaError_t launch_mla_combine(int total_q, const MlaParams& p, cudaStream_t stream);
+
+// -------------------------------------------------------------- dense MLA --
+struct DenseMlaParams {
+  const int32_t* cu_q = nullptr;
+  const int32_t* kv_len = nullptr;
+  const int64_t* kv_start = nullptr;
+  PageTable pt;
+  int64_t total_keys = 0;
+  int32_t total_q = 0;
+  int32_t num_seqs = 0;
+  int32_t max_kv_len = 0;
+  int32_t n_heads = 0;
+  int32_t gang = 1;                   // CTAs that walk the same keys with neighbouring row tiles
+  int32_t shared = 0;                 // the first prefix_len positions are sequence 0's for every sequence
+  int32_t prefix_len = 0;
+  float scale_log2 = 0.f;             // sm_scale * log2(e)
+  uint16_t* out = nullptr;            // bf16 [total_q, H, 512]
+  float* lse = nullptr;               // [total_q, H] or nullptr
+  int4* rec = nullptr;                // [1 + shared, total_q * H]: partial slot (-1: none), pieces, row in it, gang
+  float* part_lse = nullptr;          // [2 * kDenseMaxCtas, N] log2 units
+  float* part_o = nullptr;            // [2 * kDenseMaxCtas, N, 512] normalised
+  float* row_lse = nullptr;           // shared: [2, total_q * H] of whole items, log2 units
+  float* row_o = nullptr;             // shared: [2, total_q * H, 512]
+  uint32_t* err = nullptr;
+  long long budget = 2000000000LL;
+};
+constexpr int kDenseMaxCtas = 148;
+// Query rows per item (16, 32 or 64) and CTAs per gang for a batch.
+struct DensePlan {
+  int n;
+  int gang;
+};
+DensePlan dense_plan(const dsa_batch_t* b, int n_heads, bool shared);
+// The attention and the merge of its split items.  map_q: q as [total_q * H, 576],
+// box [N rows x 64]; map_c: the cache [total_keys, 576], box [64 rows x 64]; both
+// 128-byte swizzle.
+cudaError_t launch_dense_mla(const DenseMlaParams& p, const DensePlan& d, const CUtensorMap& map_q,
+                             const CUtensorMap& map_c, cudaStream_t stream);
+
+// ------------------------------------------------------------ page tables --
+struct PageTablesParams {
+  const int32_t* q_len = nullptr;
+  const int32_t* kv_before = nullptr;
+  const int32_t* free_pages = nullptr;
+  int32_t* block_table = nullptr;
+  int32_t* cu_q = nullptr;
+  int32_t* kv_len = nullptr;
+  int32_t* pos = nullptr;
+  int64_t* slots = nullptr;
+  int32_t* used = nullptr;
+  int32_t num_seqs = 0;
+  int32_t page = 0;
+  int32_t blocks = 0;
+  int32_t n_free = 0;
+  int32_t max_tokens = 0;
+  uint32_t* err = nullptr;
+};
+cudaError_t launch_page_tables(const PageTablesParams& p, cudaStream_t stream);
 
 // ------------------------------------------------------------------- prep --
 // per-128 FP8 quantiser: x bf16 [n_vec, 128] -> codes e4m3 [n_vec, 128], scales [n_vec]
