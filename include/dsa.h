@@ -308,6 +308,25 @@ DSA_API dsa_status_t dsa_prefix_mla(const dsa_batch_t* batch, int32_t prefix_len
                                     const void* kv, float sm_scale, void* out, float* lse, void* ws, size_t ws_bytes,
                                     dsa_stream_t stream);
 
+/* Dense latent attention, expanded form (prefill: with more query tokens than a
+ * few per sequence the expanded keys cost less to multiply than the latent
+ * ones).  Head h of position s has the key (kv_up[s, h, 0:128], rope[s]) and the
+ * value kv_up[s, h, 128:256], made by the caller's up-projection of the latent rows;
+ * the RoPE dims are shared by all heads and read where they are, e.g. kv + 512
+ * with rope_stride 576 in the latent cache.
+ *   q      [total_q, n_heads, 192] bf16 (128 dims, then 64 RoPE dims)
+ *   kv_up  [total_keys, n_heads, 256] bf16    rope [total_keys rows of 64] bf16,
+ *          rope_stride elements apart (>= 64, a multiple of 8), 16-byte aligned
+ *   out    [total_q, n_heads, 128] bf16       lse [total_q, n_heads] fp32 or NULL
+ *   1 <= n_heads <= 128; flat caches only (block_table != NULL is
+ *   DSA_ERR_UNSUPPORTED: the expanded rows are made for the call).
+ *   ws of DSA_OP_EXPANDED_MLA bytes.
+ * Arithmetic, masked positions, rows behind the last sequence and bad descriptors as
+ * dsa_dense_mla; a non-finite value that a row does see makes that output NaN. */
+DSA_API dsa_status_t dsa_expanded_mla(const dsa_batch_t* batch, const void* q, int32_t n_heads, const void* kv_up,
+                                      const void* rope, int64_t rope_stride, float sm_scale, void* out, float* lse,
+                                      void* ws, size_t ws_bytes, dsa_stream_t stream);
+
 /* The arrays of a paged batch from the requests' lengths, on the device: each
  * of num_seqs sequences has kv_before[b] positions and takes q_len[b] new
  * tokens.  Pages are page_size rows (a positive multiple of 64); a sequence

@@ -56,6 +56,7 @@ EXPORTS = [
     "dsa_cache_write",
     "dsa_dense_mla",
     "dsa_prefix_mla",
+    "dsa_expanded_mla",
     "dsa_page_tables",
 ]
 
@@ -131,6 +132,8 @@ def _lib():
         lib.dsa_dense_mla.restype = ctypes.c_int
         lib.dsa_prefix_mla.argtypes = [BP, I32, P, I32, P, F, P, P, P, SZ, P]
         lib.dsa_prefix_mla.restype = ctypes.c_int
+        lib.dsa_expanded_mla.argtypes = [BP, P, I32, P, P, I64, F, P, P, P, SZ, P]
+        lib.dsa_expanded_mla.restype = ctypes.c_int
         lib.dsa_page_tables.argtypes = [I32, P, P, P, I32, I32, P, I32, I32, P, P, P, P, P, P, SZ, P]
         lib.dsa_page_tables.restype = ctypes.c_int
         _LIB = lib
@@ -303,6 +306,22 @@ def prefix_mla(batch: Batch, prefix_len: int, q, kv, sm_scale: float, out, lse, 
     _check_cache("prefix_mla", batch, kv)
     _check(_lib().dsa_prefix_mla(batch.ref, int(prefix_len), _ptr(q), n_heads, _ptr(kv), float(sm_scale), _ptr(out),
                                  _ptr(lse), _ptr(ws), ws.numel(), _stream(stream)), "dsa_prefix_mla")
+
+
+def expanded_mla(batch: Batch, q, kv_up, rope, sm_scale: float, out, lse, ws, stream=None):
+    """Latent attention in the expanded form: q [total_q, heads, 192], kv_up [total_keys, heads, 256] (128 key dims, then
+    128 value dims), rope [total_keys, 64] (rows may lie apart, e.g. latent[:, 512:]) -> out [total_q, heads, 128],
+    lse or None; flat caches; ws of OP_EXPANDED_MLA."""
+    n_heads = _check_mla("expanded_mla", batch, q, 192, out, 128, lse)
+    if kv_up.dtype != torch.bfloat16 or kv_up.dim() != 3 or tuple(kv_up.shape[1:]) != (n_heads, 256) \
+            or kv_up.shape[0] < batch.c.total_keys or rope.dtype != torch.bfloat16 or rope.dim() != 2 \
+            or rope.shape[1] != 64 or rope.shape[0] < batch.c.total_keys or rope.stride(1) != 1:
+        raise ValueError("expanded_mla: kv_up bf16 [total_keys, heads, 256], rope bf16 [total_keys, 64]")
+    # a single row has no stride of its own
+    stride = int(rope.stride(0)) if rope.shape[0] > 1 else max(64, int(rope.stride(0)) // 8 * 8)
+    _check(_lib().dsa_expanded_mla(batch.ref, _ptr(q), n_heads, _ptr(kv_up), ctypes.c_void_p(rope.data_ptr()), stride,
+                                   float(sm_scale), _ptr(out), _ptr(lse), _ptr(ws), ws.numel(), _stream(stream)),
+           "dsa_expanded_mla")
 
 
 def page_tables(q_len, kv_before, free_pages, page_size: int, block_table, cu_q, kv_len, pos, slots, pages_used, ws,

@@ -107,6 +107,47 @@ dsa_status_t dsa_prefix_mla(const dsa_batch_t* batch, int32_t prefix_len, const 
                    reinterpret_cast<cudaStream_t>(stream));
 }
 
+dsa_status_t dsa_expanded_mla(const dsa_batch_t* b, const void* q, int32_t n_heads, const void* kv_up, const void* rope,
+                              int64_t rope_stride, float sm_scale, void* out, float* lse, void* ws, size_t ws_bytes,
+                              dsa_stream_t stream) {
+  const dsa_status_t s = dsa::validate_batch(b);
+  if (s != DSA_OK) return s;
+  if (q == nullptr || kv_up == nullptr || rope == nullptr || out == nullptr) return DSA_ERR_INVALID_ARG;
+  if (misaligned(q, 16) || misaligned(kv_up, 16) || misaligned(rope, 16) || misaligned(out, 16) || misaligned(lse, 4))
+    return DSA_ERR_INVALID_ARG;
+  if (rope_stride < 64 || rope_stride % 8 != 0 || rope_stride >= (int64_t(1) << 31)) return DSA_ERR_INVALID_ARG;
+  if (!(sm_scale > 0.f) || !std::isfinite(sm_scale)) return DSA_ERR_INVALID_ARG;
+  if (n_heads < 1 || n_heads > 128 || b->block_table != nullptr) return DSA_ERR_UNSUPPORTED;
+  if (ws == nullptr || misaligned(ws, 16)) return DSA_ERR_INVALID_ARG;
+  if (ws_bytes < kHeader) return DSA_ERR_WORKSPACE;
+  if (b->total_q == 0) return DSA_OK;
+  dsa::ExpandedMlaParams p;
+  p.cu_q = b->cu_q;
+  p.kv_len = b->kv_len;
+  p.kv_start = b->kv_start;
+  p.total_keys = b->total_keys;
+  p.total_q = b->total_q;
+  p.num_seqs = b->num_seqs;
+  p.max_kv_len = b->max_kv_len;
+  p.n_heads = n_heads;
+  p.scale_log2 = static_cast<float>(static_cast<double>(sm_scale) * 1.4426950408889634);
+  p.out = static_cast<uint16_t*>(out);
+  p.lse = lse;
+  p.err = static_cast<uint32_t*>(ws);
+  p.budget = dsa::wait_budget();
+  const uint64_t h = static_cast<uint64_t>(n_heads);
+  CUtensorMap map_q, map_kv, map_r;
+  if (!dsa::make_tmap_bf16(&map_q, q, static_cast<uint64_t>(b->total_q), h * 192, h * 192, 128) ||
+      !dsa::make_tmap_bf16(&map_kv, kv_up, static_cast<uint64_t>(b->total_keys), h * 256, h * 256, 128) ||
+      !dsa::make_tmap_bf16(&map_r, rope, static_cast<uint64_t>(b->total_keys), 64, static_cast<uint64_t>(rope_stride),
+                           128))
+    return DSA_ERR_CUDA;
+  return dsa::launch_expanded_mla(p, b->max_q_per_seq, map_q, map_kv, map_r, reinterpret_cast<cudaStream_t>(stream)) ==
+                 cudaSuccess
+             ? DSA_OK
+             : DSA_ERR_CUDA;
+}
+
 dsa_status_t dsa_page_tables(int32_t num_seqs, const int32_t* q_len, const int32_t* kv_before,
                              const int32_t* free_pages, int32_t n_free, int32_t page_size, int32_t* block_table,
                              int32_t blocks_per_seq, int32_t max_tokens, int32_t* cu_q, int32_t* kv_len, int32_t* pos,

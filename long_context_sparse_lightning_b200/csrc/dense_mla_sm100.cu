@@ -125,16 +125,6 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// D (TMEM) += A (shared) x B (shared), 16-bit operands.
-__device__ __forceinline__ void umma_f16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
 // 16 TMEM lanes x N columns, the layout of tmem_ld_16x256b_x8
 __device__ __forceinline__ void ld_scores(uint32_t t, uint32_t (&r)[32]) { tmem_ld_16x256b_x8(t, r); }
 __device__ __forceinline__ void ld_scores(uint32_t t, uint32_t (&r)[16]) {

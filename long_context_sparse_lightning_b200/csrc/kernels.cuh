@@ -242,6 +242,27 @@ DensePlan dense_plan(const dsa_batch_t* b, int n_heads, bool shared);
 cudaError_t launch_dense_mla(const DenseMlaParams& p, const DensePlan& d, const CUtensorMap& map_q,
                              const CUtensorMap& map_c, cudaStream_t stream);
 
+// ----------------------------------------------------------- expanded MLA --
+struct ExpandedMlaParams {
+  const int32_t* cu_q = nullptr;
+  const int32_t* kv_len = nullptr;
+  const int64_t* kv_start = nullptr;
+  int64_t total_keys = 0;
+  int32_t total_q = 0;
+  int32_t num_seqs = 0;
+  int32_t max_kv_len = 0;
+  int32_t n_heads = 0;
+  float scale_log2 = 0.f;             // sm_scale * log2(e)
+  uint16_t* out = nullptr;            // bf16 [total_q, H, 128]
+  float* lse = nullptr;               // [total_q, H] or nullptr
+  uint32_t* err = nullptr;
+  long long budget = 2000000000LL;
+};
+// map_q: q as [total_q, H * 192]; map_kv: [total_keys, H * 256]; map_r: the RoPE
+// dims [total_keys, 64]; boxes of [128 rows x 64], 128-byte swizzle.
+cudaError_t launch_expanded_mla(const ExpandedMlaParams& p, int max_q_per_seq, const CUtensorMap& map_q,
+                                const CUtensorMap& map_kv, const CUtensorMap& map_r, cudaStream_t stream);
+
 // ------------------------------------------------------------ page tables --
 struct PageTablesParams {
   const int32_t* q_len = nullptr;

@@ -325,6 +325,16 @@ __device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, ui
       : "memory");
 }
 
+// D (TMEM) += A (shared) x B (shared), 16-bit operands.
+__device__ __forceinline__ void umma_f16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
 // 16 TMEM lanes x 64 columns (shape .16x256b, 8 repetitions of 8 columns).
 // Thread t holds, for repetition k: r[4k], r[4k+1] = lane t/4, columns 8k + 2(t%4) + {0, 1};
 // r[4k+2], r[4k+3] = lane t/4 + 8, the same columns.

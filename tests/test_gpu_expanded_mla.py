@@ -1,0 +1,124 @@
+"""Latent attention in the expanded form (dsa_expanded_mla) against its definition in 64 bits."""
+
+import pytest
+import torch
+
+import long_context_sparse_lightning_b200 as dsa
+from tests.dense_ref import Case, check
+
+pytestmark = pytest.mark.gpu
+
+
+class Expanded(Case):
+    """Case with per-head keys and values; rows that no sequence owns are NaN."""
+
+    def __init__(self, q_len, kv_len, heads, seed=0, **kw):
+        super().__init__(q_len, kv_len, heads, 0, seed=seed, q_dim=192, **kw)
+        self.up = torch.full((self.total_keys, heads, 256), float("nan"), dtype=torch.bfloat16)
+        self.up[self.used] = torch.randn((len(self.used), heads, 256), generator=self.g).to(torch.bfloat16)
+
+    def run(self, check=True, contiguous_rope=False):
+        out, lse = self.outputs(128)
+        ws = dsa.workspace(dsa.OP_EXPANDED_MLA, self.batch, n_heads=self.heads)
+        rope = self.cache.cuda()[:, 512:]
+        if contiguous_rope:
+            rope = rope.contiguous()
+        dsa.expanded_mla(self.batch, self.q.cuda(), self.up.cuda(), rope, self.scale, out, lse, ws)
+        if check:
+            dsa.check_device_error(ws)
+        return out.cpu(), lse.cpu()
+
+    def exact_expanded(self):
+        def kv(b):
+            up = self.up[self.at[b]].double()
+            r = self.cache[self.at[b], 512:].double()[:, None, :].expand(-1, self.heads, -1)
+            return torch.cat([up[..., :128], r], -1), up[..., 128:]
+        return self.exact(kv)
+
+
+CASES = [
+    # (q_len, kv_len, heads)
+    ([1], [1], 1),
+    ([1], [129], 3),
+    ([128], [128], 2),
+    ([129], [129], 2),
+    ([256], [256], 1),
+    ([257, 3], [300, 1000], 2),
+    ([5, 0, 130], [5, 40, 200], 3),
+    ([700], [1500], 2),
+    ([100, 300, 1, 513], [100, 333, 513, 640], 4),
+    ([64], [2000], 16),
+    ([30], [30], 128),
+]
+
+
+@pytest.mark.parametrize("q,kv,heads", CASES)
+def test_expanded_against_64_bits(q, kv, heads):
+    c = Expanded(q, kv, heads, seed=1, pad_rows=3)
+    out, lse = c.run(contiguous_rope=heads % 2 == 0)
+    check(out, lse, c.exact_expanded(), c.rows)
+
+
+def test_growing_scores():
+    for sign in (1.0, -1.0):
+        c = Expanded([300], [900], 2, seed=2)
+        c.up[c.at[0], :, 5] = (sign * torch.arange(900).float() / 900 * 600).to(torch.bfloat16)[:, None]
+        c.q[:, :, 5] = 8.0
+        out, lse = c.run()
+        check(out, lse, c.exact_expanded(), c.rows)
+
+
+def test_values_at_positions_later_tokens_alone_see():
+    c = Expanded([300], [300], 1, seed=3)
+    want = c.exact_expanded()
+    row = c.at[0][200]
+    c.up[row, 0, 128 + 9] = float("nan")          # a value of position 200, dim 9
+    c.up[row + 50, 0, 3] = float("inf")           # a key of position 250
+    out, _ = c.run()
+    got = out[:300, 0].float()
+    assert torch.isfinite(got[:200]).all()
+    assert torch.isnan(got[200:, 9]).all()
+    assert torch.isfinite(got[200:250][:, [d for d in range(128) if d != 9]]).all()
+    d = (got[:200].double() - want[0][:200, 0]).abs()
+    A, e = want[2][:200, 0], want[3][:200, 0]
+    assert (d <= A * (2.0 ** -8 + 2 * e[:, None] + 2.0 ** -18) + 2.0 ** -8 * want[0][:200, 0].abs()).all()
+
+
+def test_bad_descriptors_are_bounds_errors():
+    c = Expanded([10, 10], [50, 60], 2, seed=4)
+    want = c.exact_expanded()
+    c.start[1] = c.total_keys - 5
+    out, lse = c.outputs(128)
+    ws = dsa.workspace(dsa.OP_EXPANDED_MLA, c.batch, n_heads=2)
+    dsa.expanded_mla(c.batch, c.q.cuda(), c.up.cuda(), c.cache.cuda()[:, 512:], c.scale, out, lse, ws)
+    with pytest.raises(dsa.DSAError) as e:
+        dsa.check_device_error(ws)
+    assert e.value.status == 6
+    assert (out[10:20] == 0).all() and torch.isneginf(lse[10:20]).all()
+    assert (out[:10].cpu().double() - want[0][:10]).norm() <= 2.0 ** -8 * want[0][:10].norm()
+
+
+def test_equals_the_absorbed_form():
+    # keys and values made from the latent rows by up-projections, and the same
+    # projections absorbed into q and applied to the absorbed output
+    heads, n = 4, 200
+    c = Case([n], [n], heads, 0, seed=5, q_dim=192)
+    g = torch.Generator().manual_seed(6)
+    wk = torch.randn((heads, 128, 512), generator=g) / 512 ** 0.5
+    wv = torch.randn((heads, 128, 512), generator=g) / 512 ** 0.5
+    lat = c.cache.nan_to_num().double()
+    up = torch.cat([torch.einsum("hdc,sc->shd", wk.double(), lat[:, :512]),
+                    torch.einsum("hdc,sc->shd", wv.double(), lat[:, :512])], -1).to(torch.bfloat16)
+    qa = torch.cat([torch.einsum("ihd,hdc->ihc", c.q[..., :128].double(), wk.double()), c.q[..., 128:].double()], -1)
+    out, lse = c.outputs(128)
+    ws = dsa.workspace(dsa.OP_EXPANDED_MLA, c.batch, n_heads=heads)
+    dsa.expanded_mla(c.batch, c.q.cuda(), up.cuda(), c.cache.cuda()[:, 512:], c.scale, out, lse, ws)
+    dsa.check_device_error(ws)
+    oa, la = c.outputs(512)
+    ws = dsa.workspace(dsa.OP_DENSE_MLA, c.batch, n_heads=heads)
+    dsa.dense_mla(c.batch, qa.to(torch.bfloat16).cuda(), c.cache.cuda(), c.scale, oa, la, ws)
+    dsa.check_device_error(ws)
+    o2 = torch.einsum("ihc,hdc->ihd", oa.cpu().double(), wv.double())
+    # per form: the operands' rounding (keys, values or absorbed q: 2^-8 each, which moves a score of size
+    # |q||k| scale ~ 1 by as much), the probabilities' and the output's: six half steps in all, in the 2-norm
+    assert (out.cpu().double() - o2).norm() <= 6 * 2.0 ** -8 * o2.norm()
