@@ -25,7 +25,7 @@ struct DenseLayout {
 DenseLayout dense_layout(const dsa_batch_t* b, int n_heads, bool shared) {
   const dsa::DensePlan d = dsa::dense_plan(b, n_heads, shared);
   const size_t rows = static_cast<size_t>(b->total_q) * n_heads, halves = shared ? 2 : 1;
-  const size_t slots = static_cast<size_t>(2 * dsa::kDenseMaxCtas) * d.n;
+  const size_t slots = static_cast<size_t>(dsa::dense_slots(d.n)) * d.n;
   DenseLayout l;
   l.rec = kHeader;
   l.part_lse = l.rec + round_up(halves * rows * sizeof(int4), 256);
@@ -77,8 +77,9 @@ dsa_status_t run_dense(const dsa_batch_t* b, int prefix_len, const void* q, int 
   p.err = reinterpret_cast<uint32_t*>(base);
   p.budget = dsa::wait_budget();
   CUtensorMap map_q, map_c;
-  if (!dsa::make_tmap_bf16(&map_q, q, static_cast<uint64_t>(b->total_q) * n_heads, 576, 576, d.n) ||
-      !dsa::make_tmap_bf16(&map_c, kv, static_cast<uint64_t>(b->total_keys), 576, 576, 64))
+  if (!dsa::make_tmap_bf16(&map_q, q, static_cast<uint64_t>(b->total_q) * n_heads, 576, 576,
+                           dsa::dense_q_box(d.n)) ||
+      !dsa::make_tmap_bf16(&map_c, kv, static_cast<uint64_t>(b->total_keys), 576, 576, dsa::dense_c_box(d.n)))
     return DSA_ERR_CUDA;
   return dsa::launch_dense_mla(p, d, map_q, map_c, stream) == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 }

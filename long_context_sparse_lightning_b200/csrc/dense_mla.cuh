@@ -1,0 +1,309 @@
+// What the two dense latent attention kernels share: the work list (sequences, or a
+// shared prefix and then the sequences' own parts, cut into items of N query
+// rows and laid end to end by their tile counts), the walk of one unit's equal
+// share of it, and small helpers.  A unit is a CTA or a CTA pair; W units form a
+// gang that walks the same keys with neighbouring row tiles.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "kernels.cuh"
+#include "ptx.cuh"
+
+namespace dsa {
+namespace dense {
+
+constexpr int kTile = 64;                 // keys per tile
+constexpr float kGrow = 24.f;             // log2 units a score may exceed its row's reference by
+constexpr int kItemCost = 2;              // an item's prologue and epilogue, in tiles
+constexpr int kMinShare = 2;              // tiles (and item costs) a gang takes at least
+constexpr float kLn2 = 0.69314718055994531f;
+
+struct Item {
+  int32_t n_tiles;      // -1: no more items
+  int32_t tile0;        // first tile (position / 64)
+  int32_t row0;         // first row of the item in [total_q * H]
+  int32_t rows;         // rows of the item (<= N)
+  int32_t seq_row0;     // first row of the item's sequence
+  int32_t base;         // position of the sequence's first query
+  int32_t lo;           // first position of the item (suffix of a shared prefix)
+  int32_t last;         // last position any row of the item sees
+  int32_t slot;         // partial slot, -1: the item is whole
+  int32_t pieces;       // pieces of the item (set where begins), 0: a sequence that is out of range
+  int32_t begins;
+  int32_t prefix;       // an item of the shared prefix
+};
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// The softmax warps' barrier; returns the OR of `v` over them.
+__device__ __forceinline__ bool soft_any(bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, 1, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(v ? 1u : 0u)
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ void soft_sync() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
+
+// Non-finite bf16 values become 0 (both halves of a word).
+__device__ __forceinline__ uint32_t finite_or_zero(uint32_t w) {
+  if ((w & 0x7F80u) == 0x7F80u) w &= 0xFFFF0000u;
+  if ((w & 0x7F800000u) == 0x7F800000u) w &= 0x0000FFFFu;
+  return w;
+}
+
+// Entry v of the launch's work list.  With a shared prefix entry 0 is the prefix
+// (every row of the batch, positions 0 .. prefix-1) and entry v > 0 the rest
+// of sequence v - 1; without one entry v is sequence v.
+struct Entry {
+  int row0, rows;      // rows in [total_q * H]
+  int q_len, kv;
+  int b;               // sequence (block-table row; the prefix's positions go through sequence 0's)
+  int lo;              // first position
+  int gangs;           // groups of W row tiles
+  int status;          // 0, or the error site
+  bool prefix;
+};
+
+template <int N>
+__device__ __forceinline__ Entry entry_at(const DenseMlaParams& p, int v) {
+  Entry e;
+  e.status = 0;
+  e.prefix = p.shared && v == 0;
+  const int b = p.shared ? v - 1 : v;
+  if (e.prefix) {
+    const int n = min(max(__ldg(&p.cu_q[p.num_seqs]), 0), p.total_q);
+    e.row0 = 0;
+    e.rows = p.prefix_len > 0 ? n * p.n_heads : 0;
+    e.q_len = n;
+    e.kv = p.prefix_len;
+    e.b = 0;
+    e.lo = 0;
+  } else {
+    const int q0 = __ldg(&p.cu_q[b]), q1 = __ldg(&p.cu_q[b + 1]);
+    e.b = b;
+    e.kv = __ldg(&p.kv_len[b]);
+    e.lo = p.shared ? p.prefix_len : 0;
+    if (q0 < 0 || q1 < q0 || q1 > p.total_q || (b == 0 && q0 != 0)) {   // no rows of q: nothing is read or written
+      e.row0 = e.rows = e.q_len = 0;
+      e.status = 501;
+    } else {
+      e.row0 = q0 * p.n_heads;
+      e.q_len = q1 - q0;
+      e.rows = e.q_len * p.n_heads;
+      const int64_t ks = seq_start(p.pt, p.kv_start, b);
+      if (e.q_len > e.kv || e.kv > p.max_kv_len || !seq_rows_ok(p.pt, ks, e.kv, p.total_keys))
+        e.status = 502;
+      else if (e.q_len > 0 && e.kv - e.q_len < e.lo)
+        e.status = 503;                             // the sequence does not hold the whole prefix
+    }
+  }
+  e.gangs = (e.rows + N * p.gang - 1) / (N * p.gang);
+  return e;
+}
+
+// Last position the rows [.., row_end) of the entry see.
+__device__ __forceinline__ int last_seen(const DenseMlaParams& p, const Entry& e, int row_end) {
+  if (e.prefix) return e.kv - 1;
+  return e.kv - e.q_len + (row_end - 1) / p.n_heads;
+}
+
+// Tiles of gang g of the entry (0 for an entry that is out of range).
+template <int N>
+__device__ __forceinline__ int gang_tiles(const DenseMlaParams& p, const Entry& e, int g) {
+  if (e.status != 0) return 0;
+  const int end = min(e.rows, (g + 1) * N * p.gang);
+  return last_seen(p, e, end) / kTile + 1 - e.lo / kTile;
+}
+
+template <int N>
+__device__ __forceinline__ long long entry_cost(const DenseMlaParams& p, int v) {
+  const Entry e = entry_at<N>(p, v);
+  if (e.prefix || e.gangs <= 1 || e.status != 0)
+    return e.gangs > 0 ? static_cast<long long>(e.gangs) * (gang_tiles<N>(p, e, 0) + kItemCost) : 0;
+  long long c = 0;
+  for (int g = 0; g < e.gangs; ++g) c += gang_tiles<N>(p, e, g) + kItemCost;
+  return c;
+}
+
+// One gang's share [lo, hi) of the line of `total`, and where it begins.
+struct Share {
+  long long total, lo, hi, start;      // start: of entry `entry` on the line
+  int entry, gang, gangs, member;
+};
+
+// Shared memory of find_share.
+struct ShareScratch {
+  long long scan[8];
+  long long start;
+  int32_t entry;
+};
+
+// Called by every thread of the block (THREADS <= 256); unit of n_units.
+template <int N, int THREADS>
+__device__ __forceinline__ Share find_share(const DenseMlaParams& p, ShareScratch& sc, int unit, int n_units) {
+  constexpr int WARPS = THREADS / 32;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int n_entries = p.num_seqs + (p.shared ? 1 : 0);
+  long long mine = 0;
+  for (int v = tid; v < n_entries; v += THREADS) mine += entry_cost<N>(p, v);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+  if (lane == 0) sc.scan[warp] = mine;
+  if (tid == 0) sc.entry = -1;
+  __syncthreads();
+  Share s;
+  s.total = 0;
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w) s.total += sc.scan[w];
+  s.gang = unit / p.gang;
+  s.member = unit % p.gang;
+  s.gangs = static_cast<int>(
+      min(static_cast<long long>(n_units / p.gang), max(1LL, (s.total + kMinShare - 1) / kMinShare)));
+  s.lo = s.gang < s.gangs ? s.total * s.gang / s.gangs : s.total;
+  s.hi = s.gang < s.gangs ? s.total * (s.gang + 1) / s.gangs : s.total;
+  __syncthreads();
+  if (s.lo < s.hi) {
+    long long base = 0;
+    for (int v0 = 0; v0 < n_entries; v0 += THREADS) {
+      const int v = v0 + tid;
+      const long long c = v < n_entries ? entry_cost<N>(p, v) : 0;
+      long long inc = c;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long t = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += t;
+      }
+      if (lane == 31) sc.scan[warp] = inc;
+      __syncthreads();
+      long long before = base, all = 0;
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) {
+        if (w < warp) before += sc.scan[w];
+        all += sc.scan[w];
+      }
+      const long long start = before + inc - c;
+      if (c > 0 && start <= s.lo && s.lo < start + c) {
+        sc.entry = v;
+        sc.start = start;
+      }
+      base += all;
+      __syncthreads();
+      if (base > s.lo) break;      // uniform
+    }
+  }
+  s.entry = s.lo < s.hi ? sc.entry : -1;
+  s.start = s.entry >= 0 ? sc.start : 0;
+  return s;
+}
+
+// The pieces of a share, in order (one warp, every lane the same).
+template <int N>
+struct Walk {
+  const DenseMlaParams& p;
+  const Share sh;
+  int unit, v, g = 0;
+  long long at, start;                 // position on the line, start of gang g of entry v
+  Entry e;
+
+  __device__ __forceinline__ Walk(const DenseMlaParams& p_, const Share& s, int unit_)
+      : p(p_), sh(s), unit(unit_), v(s.entry), at(s.lo), start(s.start) {
+    if (v >= 0) e = entry_at<N>(p, v);
+  }
+
+  // The next piece; false at the end of the share.
+  __device__ __forceinline__ bool next(Item& it) {
+    const int n_entries = p.num_seqs + (p.shared ? 1 : 0);
+    while (v >= 0 && v < n_entries && at < sh.hi) {
+      const int nt = gang_tiles<N>(p, e, g);
+      const long long end = start + nt + kItemCost;
+      if (at >= end) {                                       // gang g lies before the share's position
+        start = end;
+        if (++g >= e.gangs) {
+          g = 0;
+          do ++v;
+          while (v < n_entries && (e = entry_at<N>(p, v)).gangs == 0);
+        }
+        continue;
+      }
+      const int t0 = static_cast<int>(min(at - start, static_cast<long long>(nt)));
+      const int t1 = static_cast<int>(min(sh.hi - start, static_cast<long long>(nt)));
+      const bool begins = at == start;
+      at = min(sh.hi, end);
+      if (!begins && t0 == t1) continue;                     // only the item's constant cost is left
+      const int first = (g * p.gang + sh.member) * N;        // row tile of this member
+      if (first >= e.rows) continue;
+      it.rows = min(N, e.rows - first);
+      it.row0 = e.row0 + first;
+      it.seq_row0 = e.row0;
+      it.base = e.kv - e.q_len;
+      it.lo = e.lo;
+      it.prefix = e.prefix ? 1 : 0;
+      it.begins = begins ? 1 : 0;
+      it.pieces = 0;
+      it.last = -1;
+      it.tile0 = e.lo / kTile + t0;
+      it.n_tiles = 0;
+      it.slot = -1;
+      if (e.status == 0) {
+        it.last = last_seen(p, e, first + it.rows);
+        const int own = it.last / kTile + 1 - e.lo / kTile;  // this row tile may end before the gang's last
+        it.n_tiles = max(0, min(t1, own) - t0);
+        const long long x = start + nt;                      // one past the item's last tile
+        const int g_last = static_cast<int>((x * sh.gangs - 1) / sh.total);
+        it.pieces = begins ? g_last - sh.gang + 1 : 0;
+        if (!begins || t1 < nt) it.slot = unit * 2 + (begins ? 1 : 0);
+      }
+      return true;
+    }
+    return false;
+  }
+};
+
+// Sequences that are out of range into the error word (one warp).
+template <int N>
+__device__ __forceinline__ void report_entries(const DenseMlaParams& p) {
+  const int n_entries = p.num_seqs + (p.shared ? 1 : 0);
+  for (int v = static_cast<int>(threadIdx.x & 31u); v < n_entries; v += 32) {
+    const Entry e = entry_at<N>(p, v);
+    if (e.status != 0) report_error(p.err, kDevErrBounds, e.status, e.b);
+  }
+}
+
+// Where row n of an item's log-sum-exp (log2 units) goes, and the item's record.
+__device__ __forceinline__ void store_lse(const DenseMlaParams& p, const Item& it, int N, int n, float lse2) {
+  const int64_t rows = static_cast<int64_t>(p.total_q) * p.n_heads, r = it.row0 + n;
+  if (it.slot >= 0) {
+    p.part_lse[static_cast<int64_t>(it.slot) * N + n] = lse2;
+  } else if (p.shared) {
+    p.row_lse[(it.prefix ? 0 : rows) + r] = lse2;
+  } else if (p.lse != nullptr) {
+    p.lse[r] = lse2 * kLn2;
+  }
+  if (it.begins) p.rec[(p.shared && !it.prefix ? rows : 0) + r] = make_int4(it.slot, it.pieces, n, p.gang);
+}
+
+// fp32 destination of the item's rows (row n at + n * 512), null: the bf16 output.
+__device__ __forceinline__ float* fp32_rows(const DenseMlaParams& p, const Item& it, int N) {
+  if (it.slot >= 0) return p.part_o + static_cast<int64_t>(it.slot) * N * 512;
+  if (p.shared) return p.row_o + (static_cast<int64_t>(it.prefix ? 0 : 1) * p.total_q * p.n_heads + it.row0) * 512;
+  return nullptr;
+}
+
+}  // namespace dense
+}  // namespace dsa

@@ -1,0 +1,522 @@
+// Dense latent attention in the absorbed form for many query rows: a CTA pair
+// per item of 128 rows (heads of a token, or of several), tcgen05 cta_group::2.
+//
+//     S [128 x 64]   = Q [128 x 576] . C^T            (M = 128, N = 64,  K = 576)
+//     O [128 x 512] += P [128 x 64] . C[:, 0:512]     (M = 128, N = 256 twice, K = 64)
+//
+// Each CTA holds 64 of the rows (all of Q, P and its half of the accumulators),
+// so softmax needs no exchange, and half of every B operand, which the tensor
+// cores of both read: for S the keys [32 r, 32 r + 32) of a tile with all 576
+// dims, for O the dims [256 r, 256 r + 256) with all 64 keys.  An M = 128 product of a
+// pair runs at the full rate (measured: 65 cycles for N = 256, K = 16; one CTA with 64
+// rows gets half of that), where the transposed form of the one-CTA kernel
+// pays 34 + 48 cycles for the same work.
+//
+// A descriptor of a pair names one offset for both CTAs, which ties the two
+// uses of a tile together: block d of a tile's stage holds this CTA's own keys
+// at dims [64 d, 64 d + 64) while S reads it.  Then the four blocks of the other
+// CTA's dims are no longer needed, and the keys of the other CTA at this CTA's own
+// dims are loaded over them: blocks 0-3 become the keys 0-31 and blocks 4-7 the keys
+// 32-63, each CTA's own dims, at the same offsets in both.  A tile costs 9 + 4
+// blocks of 4 KB per CTA and four tiles fit beside Q (with the second four in
+// blocks of their own it would be three, and a wait between S and O is
+// covered by the next tile's S anyway).
+//
+// Tensor memory of one CTA (M = 128 over a pair: lanes 0-63 hold the rows'
+// first N / 2 columns, lanes 64-127 the others): O at [0, 256), two score
+// buffers of 32 columns.
+//
+// Roles per CTA: warp 0 items and TMA of the keys, warp 1 MMAs (rank 0), warp 2
+// TMA of the second half, warps 4-7 softmax and epilogue (thread = one row's
+// 32 keys of a tile, or 256 of its output dims).  Row references as in the one-CTA kernel.
+#include <atomic>
+
+#include "dense_mla.cuh"
+
+namespace dsa {
+namespace {
+
+using namespace dense;
+
+constexpr int kN = 128;                   // rows per item
+constexpr int kThreads = 256;
+constexpr int kBlk = 32 * 128;            // [32 keys x 64 dims]
+constexpr int kStage = 9 * kBlk;
+constexpr int kStages = 4;
+constexpr int kQBlk = 64 * 128;           // [64 rows x 64 dims]
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t TM_S = 256;            // + 32 * buffer
+
+constexpr int OFF_Q = 0;
+constexpr int OFF_P = 9 * kQBlk;          // [64 rows x 64 keys] bf16
+constexpr int OFF_KV = OFF_P + kQBlk;
+constexpr int OFF_AUX = OFF_KV + kStages * kStage;
+constexpr int kSmem = OFF_AUX + 2048 + 1024;
+static_assert(kSmem <= 232448, "shared memory of one CTA");
+static_assert(OFF_KV % 1024 == 0 && kStage % 1024 == 0, "swizzle atoms");
+
+struct Aux {
+  uint64_t q_full, q_free;
+  uint64_t full[kStages], empty[kStages];   // keys landed in both CTAs (rank 0's) / tile done (both)
+  uint64_t rows_set[kStages];               // this stage's cache row is known (for warp 2)
+  uint64_t v_full[kStages];                 // the other CTA's keys landed here
+  uint64_t s_full[2], s_free[2];
+  uint64_t p_full;
+  uint64_t o_full, o_free;
+  uint64_t item_full[2], item_free[2];
+  Item item[2];
+  int32_t row[kStages];                     // cache row of the tile's position 0, -1: a page outside the pool
+  uint32_t tmem;
+  union {
+    ShareScratch share;
+    float mx[2][64];                        // per half of a tile's keys: row maxima / row sums
+  };
+};
+static_assert(sizeof(Aux) <= 2048, "");
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    dense_pair_kernel(const DenseMlaParams p, const __grid_constant__ CUtensorMap map_q,
+                      const __grid_constant__ CUtensorMap map_c) {
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  uint8_t* sm = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+  Aux* ax = reinterpret_cast<Aux*>(sm + OFF_AUX);
+  const uint32_t rank = cluster_ctarank();
+  const int unit = static_cast<int>(blockIdx.x >> 1), n_units = static_cast<int>(gridDim.x >> 1);
+  const uint32_t warp = warp_id(), lane = lane_id();
+  const int tid = threadIdx.x;
+  const int H = p.n_heads;
+
+  if (tid == 0) {
+    mbar_init(&ax->q_full, 1);
+    mbar_init(&ax->q_free, 1);
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&ax->full[i], 1);
+      mbar_init(&ax->empty[i], 1);
+      mbar_init(&ax->rows_set[i], 1);
+      mbar_init(&ax->v_full[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ax->s_full[i], 1);
+      mbar_init(&ax->s_free[i], 8);                    // softmax warps of both CTAs
+      mbar_init(&ax->item_full[i], 1);
+      mbar_init(&ax->item_free[i], rank == 0 ? 6 : 5); // softmax warps, warp 2, rank 0's MMA thread
+    }
+    mbar_init(&ax->p_full, 8);
+    mbar_init(&ax->o_full, 1);
+    mbar_init(&ax->o_free, 8);
+    fence_mbar_init();
+    prefetch_tmap(&map_q);
+    prefetch_tmap(&map_c);
+  }
+  if (warp == 1) tmem_alloc_pair(&ax->tmem, kTmemCols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const Share share = find_share<kN, kThreads>(p, ax->share, unit, n_units);
+  __syncthreads();
+  cluster_sync();                                      // the other CTA's barriers exist
+  const uint32_t tmem = ax->tmem;
+
+  if (warp == 0) {
+    // ------------------------------------------- items, rows and keys by TMA --
+    bool ok = true;
+    auto wait = [&](uint64_t* b, uint32_t parity, uint32_t site) {
+      if (ok && !mbar_wait(b, parity, p.budget)) {
+        if (lane == 0) report_error(p.err, kDevErrTimeout, site, blockIdx.x);
+        ok = false;
+      }
+      ok = __all_sync(0xffffffffu, ok);
+    };
+    if (blockIdx.x == 0) report_entries<kN>(p);
+    int k = 0, n_q = 0, t = 0;
+    auto publish = [&](const Item& it) {
+      if (k >= 2) wait(&ax->item_free[k & 1], ((k >> 1) + 1) & 1, 550);
+      if (ok && lane == 0) {
+        ax->item[k & 1] = it;
+        mbar_arrive(&ax->item_full[k & 1]);
+      }
+      __syncwarp();
+      ++k;
+    };
+    const uint32_t q_full = mapa_shared(smem_u32(&ax->q_full), 0);
+    Walk<kN> walk(p, share, unit);
+    Item it;
+    while (ok && walk.next(it)) {
+      publish(it);
+      if (!ok || it.n_tiles == 0) continue;
+      if (n_q > 0) wait(&ax->q_free, (n_q - 1) & 1, 551);
+      if (!ok) break;
+      ++n_q;
+      if (lane == 0) {
+        if (rank == 0) mbar_arrive_expect_tx(&ax->q_full, 2 * 9 * kQBlk);
+        for (int c = 0; c < 9; ++c)
+          tma_load_2d_pair(sm + OFF_Q + c * kQBlk, &map_q, q_full, c * 64, it.row0 + 64 * static_cast<int>(rank));
+      }
+      __syncwarp();
+      const int64_t kstart = seq_start(p.pt, p.kv_start, walk.e.b);
+      int my_row = 0;
+      for (int i = 0; ok && i < it.n_tiles; ++i, ++t) {
+        if ((i & 31) == 0) {            // cache rows of the next 32 tiles, one per lane (a tile lies in one page)
+          const int u = min(i + static_cast<int>(lane), it.n_tiles - 1);
+          const int64_t r = cache_row(p.pt, walk.e.b, kstart, (it.tile0 + u) * kTile);
+          if (r < 0 && rank == 0) report_error(p.err, kDevErrBounds, 504, walk.e.b);
+          my_row = r < 0 ? -1 : static_cast<int>(r);
+        }
+        const int row = __shfl_sync(0xffffffffu, my_row, i & 31);
+        const int s = t % kStages;
+        if (t >= kStages) wait(&ax->empty[s], ((t / kStages) + 1) & 1, 552);
+        if (!ok) break;
+        if (lane == 0) {
+          ax->row[s] = row;
+          mbar_arrive(&ax->rows_set[s]);
+          if (rank == 0) mbar_arrive_expect_tx(&ax->full[s], 2 * kStage);
+          const uint32_t full = mapa_shared(smem_u32(&ax->full[s]), 0);
+          // a tile of a page outside the pool lies behind the cache: zeros arrive, no row is read
+          const int y = row < 0 ? static_cast<int>(p.total_keys) : row + 32 * static_cast<int>(rank);
+          for (int d = 0; d < 9; ++d) tma_load_2d_pair(sm + OFF_KV + s * kStage + d * kBlk, &map_c, full, d * 64, y);
+        }
+        __syncwarp();
+      }
+    }
+    if (ok) {
+      Item end;
+      end.n_tiles = -1;
+      publish(end);
+    }
+    if (!ok && rank == 0) {
+      // a wait ran out: let the copies in flight (both CTAs') land before the blocks end
+      bool landed = true;
+      if (n_q > 0) landed = mbar_wait(&ax->q_full, (n_q - 1) & 1, p.budget);
+      for (int i = max(0, t - kStages); landed && i < t; ++i)
+        landed = mbar_wait(&ax->full[i % kStages], (i / kStages) & 1, p.budget);
+    }
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- MMAs --
+    if (rank == 0 && elect_one()) {
+      constexpr uint32_t idesc_s = idesc_f32acc(kFmtBF16, kFmtBF16, 128, 64, 0, 0);     // Q, C K-major
+      constexpr uint32_t idesc_o = idesc_f32acc(kFmtBF16, kFmtBF16, 128, 256, 0, 1);    // P K-major, C MN-major
+      const uint32_t q_addr = smem_u32(sm + OFF_Q), p_addr = smem_u32(sm + OFF_P), kv_addr = smem_u32(sm + OFF_KV);
+      bool ok = true;
+      auto wait = [&](uint64_t* b, uint32_t parity, uint32_t site) {
+        if (ok && !mbar_wait_cluster(b, parity, p.budget)) {
+          report_error(p.err, kDevErrTimeout, site, blockIdx.x);
+          ok = false;
+        }
+        return ok;
+      };
+      int n_q = 0, t_s = 0, t_o = 0, n_o = 0;
+      auto score = [&](bool last) {
+        const int s = t_s % kStages, sb = t_s & 1;
+        if (t_s >= 2 && !wait(&ax->s_free[sb], ((t_s >> 1) + 1) & 1, 561)) return;
+        if (!wait(&ax->full[s], (t_s / kStages) & 1, 562)) return;
+        tc_fence_after();
+#pragma unroll
+        for (int d = 0; d < 9; ++d)
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            umma_f16_ss_pair(tmem + TM_S + 32 * sb, smem_desc(q_addr + d * kQBlk + kk * 32, 16, 1024, kSwizzle128B),
+                             smem_desc(kv_addr + s * kStage + d * kBlk + kk * 32, 16, 1024, kSwizzle128B), idesc_s,
+                             (d | kk) ? 1u : 0u);
+        umma_commit_pair(&ax->s_full[sb]);
+        if (last) umma_commit_pair(&ax->q_free);
+        ++t_s;
+      };
+      for (int k = 0; ok; ++k) {
+        if (!wait(&ax->item_full[k & 1], (k >> 1) & 1, 560)) break;
+        const int nt = ax->item[k & 1].n_tiles;
+        mbar_arrive(&ax->item_free[k & 1]);
+        if (nt < 0) break;
+        if (nt == 0) continue;
+        if (!wait(&ax->q_full, n_q & 1, 563)) break;
+        ++n_q;
+        score(nt == 1);
+        for (int i = 0; ok && i < nt; ++i) {
+          if (i + 1 < nt) score(i + 2 == nt);
+          const int s = t_o % kStages;
+          if (!ok || !wait(&ax->p_full, t_o & 1, 564)) break;       // P written, and all keys at each CTA's dims landed
+          if (i == 0 && n_o > 0 && !wait(&ax->o_free, (n_o - 1) & 1, 565)) break;
+          tc_fence_after();
+#pragma unroll
+          for (int g = 0; g < 2; ++g)
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+              for (int j = 0; j < 2; ++j)
+                umma_f16_ss_pair(tmem + 128 * j, smem_desc(p_addr + (2 * g + kk) * 32, 16, 1024, kSwizzle128B),
+                                 smem_desc(kv_addr + s * kStage + (4 * g + 2 * j) * kBlk + kk * 2048, kBlk, 1024,
+                                           kSwizzle128B),
+                                 idesc_o, (i | g | kk) ? 1u : 0u);
+          umma_commit_pair(&ax->empty[s]);
+          ++t_o;
+          if (i + 1 == nt) umma_commit_pair(&ax->o_full);
+        }
+        ++n_o;
+      }
+    }
+  } else if (warp == 2) {
+    // ------------------------- the other CTA's keys at this CTA's dims by TMA --
+    bool ok = true;
+    int n_own = 0;          // loads issued
+    auto wait = [&](uint64_t* b, uint32_t parity, uint32_t site) {
+      if (ok && !mbar_wait(b, parity, p.budget)) {
+        if (lane == 0) report_error(p.err, kDevErrTimeout, site, blockIdx.x);
+        ok = false;
+      }
+      ok = __all_sync(0xffffffffu, ok);
+    };
+    for (int k = 0; ok; ++k) {
+      wait(&ax->item_full[k & 1], (k >> 1) & 1, 570);
+      if (!ok) break;
+      const Item it = ax->item[k & 1];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ax->item_free[k & 1]);
+      if (it.n_tiles < 0) break;
+      const int min_lim = it.prefix ? it.last : it.base + (it.row0 - it.seq_row0) / H;
+      for (int i = 0; ok && i < it.n_tiles; ++i, ++n_own) {
+        const int s = n_own % kStages, pos0 = (it.tile0 + i) * kTile;
+        wait(&ax->rows_set[s], (n_own / kStages) & 1, 571);
+        wait(&ax->s_full[n_own & 1], (n_own >> 1) & 1, 572);     // S has read the tile
+        if (!ok) break;
+        if (lane == 0) {
+          const int row = ax->row[s], none = static_cast<int>(p.total_keys);
+          const bool border = row < 0 || pos0 < it.lo || pos0 + kTile - 1 > min_lim;
+          uint8_t* st = sm + OFF_KV + s * kStage;
+          // On the border the softmax warps rewrite values (below): there both
+          // halves come anew, so that this barrier covers all they touch.
+          mbar_arrive_expect_tx(&ax->v_full[s], (border ? 8 : 4) * kBlk);
+          for (int g = 0; g < 2; ++g) {
+            if (!border && g == static_cast<int>(rank)) continue;
+            for (int c = 0; c < 4; ++c)
+              tma_load_2d(st + (4 * g + c) * kBlk, &map_c, &ax->v_full[s], 256 * static_cast<int>(rank) + 64 * c,
+                          row < 0 ? none : row + 32 * g);
+          }
+        }
+        __syncwarp();
+      }
+    }
+    if (!ok) {
+      bool landed = true;
+      for (int i = max(0, n_own - kStages); landed && i < n_own; ++i)
+        landed = mbar_wait(&ax->v_full[i % kStages], (i / kStages) & 1, p.budget);
+    }
+  } else if (warp >= 4) {
+    // ---------------------------------------------------- softmax, epilogue --
+    const int qd = static_cast<int>(warp & 3u);
+    const uint32_t t_lane = tmem + (static_cast<uint32_t>(qd * 32) << 16);
+    const int half = qd >> 1;                                      // keys 32 half .. of a tile, dims 256 half ..
+    const int r = (qd & 1) * 32 + static_cast<int>(lane);          // row of this CTA
+    const int n = 64 * static_cast<int>(rank) + r;                 // row of the item
+    const int st = tid - 128;
+    const float NEG_INF = __int_as_float(0xff800000);
+    const float scale = p.scale_log2;
+    const uint32_t p_row = smem_u32(sm + OFF_P) + r * 128;
+    const uint32_t s_free0 = mapa_shared(smem_u32(&ax->s_free[0]), 0), p_full = mapa_shared(smem_u32(&ax->p_full), 0);
+    const uint32_t o_free = mapa_shared(smem_u32(&ax->o_free), 0);
+    bool ok = true;
+    // Once a wait has run out nothing waits any more: the warps go on to the
+    // end in step (their barriers keep matching) and the error word tells.
+    auto wait = [&](uint64_t* b, uint32_t parity, uint32_t site) {
+      if (ok && !mbar_wait_cluster(b, parity, p.budget)) {
+        report_error(p.err, kDevErrTimeout, site, blockIdx.x);
+        ok = false;
+      }
+      ok = __all_sync(0xffffffffu, ok);
+    };
+    int t = 0, n_o = 0;
+    for (int k = 0;; ++k) {
+      wait(&ax->item_full[k & 1], (k >> 1) & 1, 580);
+      if (soft_any(!ok)) break;       // a warp that gave up must not leave the others at a barrier
+      const Item it = ax->item[k & 1];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ax->item_free[k & 1]);
+      if (it.n_tiles < 0) break;
+      const int min_lim = it.prefix ? it.last : it.base + (it.row0 - it.seq_row0) / H;
+      const int lim = n >= it.rows ? -1 : (it.prefix ? it.last : it.base + (it.row0 + n - it.seq_row0) / H);
+      float m = NEG_INF, l = 0.f;     // the row's reference; this thread's share of its sum
+      for (int i = 0; i < it.n_tiles; ++i, ++t) {
+        const int sb = t & 1, s = t % kStages, pos0 = (it.tile0 + i) * kTile;
+        uint32_t x[32];
+        wait(&ax->s_full[sb], (t >> 1) & 1, 581);
+        tc_fence_after();
+        tmem_ld32(t_lane + TM_S + 32 * sb, x);
+        tmem_ld_wait();
+        tc_fence_before();
+        wait(&ax->rows_set[s], (t / kStages) & 1, 586);
+        const bool skip = ax->row[s] < 0;
+        __syncwarp();
+        if (lane == 0) mbar_arrive_remote(s_free0 + 8 * sb);
+        const bool border = skip || pos0 < it.lo || pos0 + kTile - 1 > min_lim;
+        if (border) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            const int pos = pos0 + 32 * half + j;
+            if (skip || pos < it.lo || pos > lim) x[j] = __float_as_uint(NEG_INF);
+          }
+        }
+        float mx = fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1]));
+#pragma unroll
+        for (int j = 2; j < 32; ++j) mx = fmaxf(mx, __uint_as_float(x[j]));
+        mx *= scale;
+        // reference -inf: any finite score grows it, a masked one (NaN here) does not
+        if (soft_any(mx - m > kGrow)) {
+          ax->mx[half][r] = mx;
+          soft_sync();
+          const float top = fmaxf(ax->mx[0][r], ax->mx[1][r]);
+          const float f = top > m ? exp2_approx(m - top) : 1.f;
+          m = fmaxf(m, top);
+          l *= f;
+          if (i > 0) {
+            // O is idle once the previous tile's product is done
+            wait(&ax->empty[(t - 1) % kStages], ((t - 1) / kStages) & 1, 582);
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < 256; c += 32) {
+              uint32_t o[32];
+              tmem_ld32(t_lane + c, o);
+              tmem_ld_wait();
+              uint32_t a[16], b[16];
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                a[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                b[j] = __float_as_uint(__uint_as_float(o[16 + j]) * f);
+              }
+              tmem_st16(t_lane + c, a);
+              tmem_st16(t_lane + c + 16, b);
+            }
+            tmem_st_wait();
+            tc_fence_before();
+          }
+          soft_sync();                // mx may be rewritten
+        }
+        const float ref = m == NEG_INF ? 0.f : -m;
+        uint32_t pk[16];
+        float sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const float a = exp2_approx(fmaf(__uint_as_float(x[2 * j]), scale, ref));
+          const float b = exp2_approx(fmaf(__uint_as_float(x[2 * j + 1]), scale, ref));
+          sum += a + b;
+          pk[j] = pack_bf16(a, b);
+        }
+        l += sum;
+        // P is read by the previous tile's product until that is done
+        if (t > 0) wait(&ax->empty[(t - 1) % kStages], ((t - 1) / kStages) & 1, 583);
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(p_row + (((4 * half + u) ^ (r & 7)) << 4)),
+                       "r"(pk[4 * u]), "r"(pk[4 * u + 1]), "r"(pk[4 * u + 2]), "r"(pk[4 * u + 3])
+                       : "memory");
+        wait(&ax->v_full[s], (t / kStages) & 1, 584);
+        if (border) {
+          // Keys that some row must not see: 0 x a non-finite value would reach that
+          // row, so such values become 0 in the tile.  A row that does see the key
+          // has its NaN from the score.
+#pragma unroll 1
+          for (int u = st; u < 8 * kBlk / 16; u += 128) {
+            const int pos = pos0 + 32 * (u >> 10) + ((u >> 3) & 31);
+            if (pos >= it.lo && pos <= min_lim) continue;
+            uint4* w = reinterpret_cast<uint4*>(sm + OFF_KV + s * kStage) + u;
+            const uint4 a = *w;
+            const uint4 b = make_uint4(finite_or_zero(a.x), finite_or_zero(a.y), finite_or_zero(a.z), finite_or_zero(a.w));
+            if (a.x != b.x || a.y != b.y || a.z != b.z || a.w != b.w) *w = b;
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_remote(p_full);
+      }
+
+      // ---- the row's sum over both halves of the keys ----
+      ax->mx[half][r] = l;
+      soft_sync();
+      const float sum = ax->mx[0][r] + ax->mx[1][r];
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      if (half == 0 && n < it.rows) store_lse(p, it, kN, n, sum == 0.f ? NEG_INF : m + log2f(sum));
+      if (it.n_tiles > 0) {
+        wait(&ax->o_full, n_o & 1, 585);
+        ++n_o;
+        tc_fence_after();
+      }
+      float* dst32 = fp32_rows(p, it, kN);
+#pragma unroll 1
+      for (int c = 0; c < 256; c += 32) {
+        uint32_t o[32];
+        if (it.n_tiles > 0) {
+          tmem_ld32(t_lane + c, o);
+          tmem_ld_wait();
+        } else {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) o[j] = 0u;
+        }
+        const int d = 256 * half + c;
+        if (n < it.rows && dst32 != nullptr && it.n_tiles > 0) {    // an empty piece has lse = -inf, its output is not read
+#pragma unroll
+          for (int j = 0; j < 32; j += 4)
+            *reinterpret_cast<float4*>(dst32 + static_cast<int64_t>(n) * 512 + d + j) =
+                make_float4(__uint_as_float(o[j]) * inv, __uint_as_float(o[j + 1]) * inv,
+                            __uint_as_float(o[j + 2]) * inv, __uint_as_float(o[j + 3]) * inv);
+        }
+        if (n < it.rows && dst32 == nullptr) {
+#pragma unroll
+          for (int j = 0; j < 32; j += 8)
+            *reinterpret_cast<uint4*>(p.out + static_cast<int64_t>(it.row0 + n) * 512 + d + j) = make_uint4(
+                pack_bf16(__uint_as_float(o[j]) * inv, __uint_as_float(o[j + 1]) * inv),
+                pack_bf16(__uint_as_float(o[j + 2]) * inv, __uint_as_float(o[j + 3]) * inv),
+                pack_bf16(__uint_as_float(o[j + 4]) * inv, __uint_as_float(o[j + 5]) * inv),
+                pack_bf16(__uint_as_float(o[j + 6]) * inv, __uint_as_float(o[j + 7]) * inv));
+        }
+        __syncwarp();
+      }
+      if (it.n_tiles > 0) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_remote(o_free);
+      }
+      soft_sync();                    // mx may be rewritten
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();                     // the other CTA no longer touches this one's memory
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, kTmemCols);
+  }
+}
+
+// CTA pairs that can be resident at once (cached per device): every pair takes an
+// equal share, so one that waited for a free slot would double the time.
+int resident_pairs() {
+  static std::atomic<int> cache[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  const int v = cache[dev].load(std::memory_order_relaxed);
+  if (v != 0) return v - 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2, 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = static_cast<size_t>(kSmem);
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, dense_pair_kernel, &cfg) != cudaSuccess) n = 0;
+  cudaGetLastError();   // a refused query leaves no sticky error behind
+  cache[dev].store(n + 1, std::memory_order_relaxed);
+  return n;
+}
+
+}  // namespace
+
+cudaError_t launch_dense_pair(const DenseMlaParams& p, const CUtensorMap& map_q, const CUtensorMap& map_c,
+                              cudaStream_t stream) {
+  cudaError_t e = cudaFuncSetAttribute(dense_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e != cudaSuccess) return e;
+  int pairs = resident_pairs();
+  if (pairs < 1) pairs = sm_count() / 2;
+  if (pairs < 1 || pairs > kDenseMaxCtas / 2) pairs = kDenseMaxCtas / 2;
+  if (pairs < p.gang) return cudaErrorInvalidConfiguration;
+  pairs = pairs / p.gang * p.gang;
+  dense_pair_kernel<<<2 * pairs, kThreads, kSmem, stream>>>(p, map_q, map_c);
+  return cudaGetLastError();
+}
+
+}  // namespace dsa

@@ -39,26 +39,21 @@
 // barrier with an OR per tile decides.  Probabilities are rounded to bf16 for the
 // second product, whose other operand is the bf16 cache tile itself; row sums
 // are taken in fp32 before that rounding.
-#include <cuda_bf16.h>
-
-#include "kernels.cuh"
-#include "ptx.cuh"
+#include "dense_mla.cuh"
 
 namespace dsa {
 namespace {
 
-constexpr int kKeys = 64;                 // keys per tile
+using namespace dense;
+
+constexpr int kKeys = kTile;
 constexpr int kBlk = kKeys * 128;         // one [64 keys x 64 dims] block, 128-byte swizzle
 constexpr int kPair = 2 * kBlk;           // 128 value dims: one M block of the second product
 constexpr int kWarps = 6;
 constexpr int kThreads = kWarps * 32;
 constexpr int kSoftThreads = 128;
-constexpr float kGrow = 24.f;             // log2 units a score may exceed its row's reference by
-constexpr int kItemCost = 2;              // an item's prologue and epilogue, in tiles
-constexpr int kMinShare = 2;              // tiles (and item costs) a group takes at least
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t TM_S = 256;            // two score buffers of 64 columns; O^T block m at column m * N
-constexpr float kLn2 = 0.69314718055994531f;
 
 template <int N>
 struct Cfg {
@@ -77,21 +72,6 @@ struct Cfg {
   static_assert(OFF_P % 1024 == 0, "swizzle atoms");
 };
 
-struct Item {
-  int32_t n_tiles;      // -1: no more items
-  int32_t tile0;        // first tile (position / 64)
-  int32_t row0;         // first row of the item in [total_q * H]
-  int32_t rows;         // rows of the item (<= N)
-  int32_t seq_row0;     // first row of the item's sequence
-  int32_t base;         // position of the sequence's first query
-  int32_t lo;           // first position of the item (suffix of a shared prefix)
-  int32_t last;         // last position any row of the item sees
-  int32_t slot;         // partial slot, -1: the item is whole
-  int32_t pieces;       // pieces of the item (set where begins), 0: a sequence that is out of range
-  int32_t begins;
-  int32_t prefix;       // an item of the shared prefix
-};
-
 struct Aux {
   uint64_t q_full, q_free;
   uint64_t rope_full[2], rope_empty[2];
@@ -103,27 +83,14 @@ struct Aux {
   Item item[2];
   int32_t skip[10];         // the tile whose first pair has this slot lies on a page outside the pool
   uint32_t tmem;
-  long long found_start;
-  int32_t found_seq;
   union {
-    long long scan[8];      // block-wide reductions of the prologue
+    ShareScratch share;
     float mx[4][64];        // per softmax warp: row maxima / row sums
   };
   float fac[64];            // rescaling factors, inverse row sums
   int32_t lim[64];          // last position each row sees
 };
 static_assert(sizeof(Aux) <= 2048, "");
-
-__device__ __forceinline__ float exp2_approx(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
 
 // 16 TMEM lanes x N columns, the layout of tmem_ld_16x256b_x8
 __device__ __forceinline__ void ld_scores(uint32_t t, uint32_t (&r)[32]) { tmem_ld_16x256b_x8(t, r); }
@@ -148,102 +115,6 @@ __device__ __forceinline__ void ld_cols16(uint32_t t, uint32_t (&r)[16]) {
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
         "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(t));
-}
-
-// The softmax warps' barrier; returns the OR of `v` over them.
-__device__ __forceinline__ bool soft_any(bool v) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.u32 p, %1, 0;\n\t"
-      "barrier.cta.red.or.pred q, 1, 128, p;\n\t"
-      "selp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"(v ? 1u : 0u)
-      : "memory");
-  return r != 0;
-}
-__device__ __forceinline__ void soft_sync() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
-
-// Non-finite bf16 values become 0 (both halves of a word).
-__device__ __forceinline__ uint32_t finite_or_zero(uint32_t w) {
-  if ((w & 0x7F80u) == 0x7F80u) w &= 0xFFFF0000u;
-  if ((w & 0x7F800000u) == 0x7F800000u) w &= 0x0000FFFFu;
-  return w;
-}
-
-// Entry v of the launch's work list.  With a shared prefix entry 0 is the prefix
-// (every row of the batch, positions 0 .. prefix-1) and entry v > 0 the rest
-// of sequence v - 1; without one entry v is sequence v.
-struct Entry {
-  int row0, rows;      // rows in [total_q * H]
-  int q_len, kv;
-  int b;               // sequence (block-table row; the prefix's positions go through sequence 0's)
-  int lo;              // first position
-  int gangs;           // groups of W row tiles
-  int status;          // 0, or the error site
-  bool prefix;
-};
-
-template <int N>
-__device__ __forceinline__ Entry entry_at(const DenseMlaParams& p, int v) {
-  Entry e;
-  e.status = 0;
-  e.prefix = p.shared && v == 0;
-  const int b = p.shared ? v - 1 : v;
-  if (e.prefix) {
-    const int n = min(max(__ldg(&p.cu_q[p.num_seqs]), 0), p.total_q);
-    e.row0 = 0;
-    e.rows = p.prefix_len > 0 ? n * p.n_heads : 0;
-    e.q_len = n;
-    e.kv = p.prefix_len;
-    e.b = 0;
-    e.lo = 0;
-  } else {
-    const int q0 = __ldg(&p.cu_q[b]), q1 = __ldg(&p.cu_q[b + 1]);
-    e.b = b;
-    e.kv = __ldg(&p.kv_len[b]);
-    e.lo = p.shared ? p.prefix_len : 0;
-    if (q0 < 0 || q1 < q0 || q1 > p.total_q || (b == 0 && q0 != 0)) {   // no rows of q: nothing is read or written
-      e.row0 = e.rows = e.q_len = 0;
-      e.status = 501;
-    } else {
-      e.row0 = q0 * p.n_heads;
-      e.q_len = q1 - q0;
-      e.rows = e.q_len * p.n_heads;
-      const int64_t ks = seq_start(p.pt, p.kv_start, b);
-      if (e.q_len > e.kv || e.kv > p.max_kv_len || !seq_rows_ok(p.pt, ks, e.kv, p.total_keys))
-        e.status = 502;
-      else if (e.q_len > 0 && e.kv - e.q_len < e.lo)
-        e.status = 503;                             // the sequence does not hold the whole prefix
-    }
-  }
-  e.gangs = (e.rows + N * p.gang - 1) / (N * p.gang);
-  return e;
-}
-
-// Last position the rows [.., row_end) of the entry see.
-__device__ __forceinline__ int last_seen(const DenseMlaParams& p, const Entry& e, int row_end) {
-  if (e.prefix) return e.kv - 1;
-  return e.kv - e.q_len + (row_end - 1) / p.n_heads;
-}
-
-// Tiles of gang g of the entry (0 for an entry that is out of range).
-template <int N>
-__device__ __forceinline__ int gang_tiles(const DenseMlaParams& p, const Entry& e, int g) {
-  if (e.status != 0) return 0;
-  const int end = min(e.rows, (g + 1) * N * p.gang);
-  return last_seen(p, e, end) / kKeys + 1 - e.lo / kKeys;
-}
-
-template <int N>
-__device__ __forceinline__ long long entry_cost(const DenseMlaParams& p, int v) {
-  const Entry e = entry_at<N>(p, v);
-  if (e.prefix || e.gangs <= 1 || e.status != 0)
-    return e.gangs > 0 ? static_cast<long long>(e.gangs) * (gang_tiles<N>(p, e, 0) + kItemCost) : 0;
-  long long c = 0;
-  for (int g = 0; g < e.gangs; ++g) c += gang_tiles<N>(p, e, g) + kItemCost;
-  return c;
 }
 
 template <int N>
@@ -283,65 +154,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_mbar_init();
     prefetch_tmap(&map_q);
     prefetch_tmap(&map_c);
-    ax->found_seq = -1;
   }
   if (warp == 1) {
     tmem_alloc(&ax->tmem, kTmemCols);
     tmem_relinquish();
   }
 
-  // ---- this group's share of the work line ----
-  const int n_entries = p.num_seqs + (p.shared ? 1 : 0);
-  long long mine = 0;
-  for (int v = tid; v < n_entries; v += kThreads) mine += entry_cost<N>(p, v);
-  {
-    long long s = mine;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (lane == 0) ax->scan[warp] = s;
-  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  long long total = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) total += ax->scan[w];
-  const int group = static_cast<int>(blockIdx.x) / p.gang, member = static_cast<int>(blockIdx.x) % p.gang;
-  const int n_groups = static_cast<int>(
-      min(static_cast<long long>(gridDim.x / p.gang), max(1LL, (total + kMinShare - 1) / kMinShare)));
-  const long long lo = group < n_groups ? total * group / n_groups : total;
-  const long long hi = group < n_groups ? total * (group + 1) / n_groups : total;
+  const Share share = find_share<N, kThreads>(p, ax->share, static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x));
   __syncthreads();
-  // the entry that holds position lo of the line
-  if (lo < hi) {
-    long long base = 0;
-    for (int v0 = 0; v0 < n_entries; v0 += kThreads) {
-      const int v = v0 + tid;
-      const long long c = v < n_entries ? entry_cost<N>(p, v) : 0;
-      long long inc = c;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long t = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= static_cast<uint32_t>(o)) inc += t;
-      }
-      if (lane == 31) ax->scan[warp] = inc;
-      __syncthreads();
-      long long before = base, all = 0;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        if (w < static_cast<int>(warp)) before += ax->scan[w];
-        all += ax->scan[w];
-      }
-      const long long start = before + inc - c;
-      if (c > 0 && start <= lo && lo < start + c) {
-        ax->found_seq = v;
-        ax->found_start = start;
-      }
-      base += all;
-      __syncthreads();
-      if (base > lo) break;      // uniform
-    }
-  }
   const uint32_t tmem = ax->tmem;
 
   if (warp == 0) {
@@ -354,11 +177,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       ok = __all_sync(0xffffffffu, ok);
     };
-    if (blockIdx.x == 0)      // sequences that are out of range, once per launch
-      for (int v = static_cast<int>(lane); v < n_entries; v += 32) {
-        const Entry e = entry_at<N>(p, v);
-        if (e.status != 0) report_error(p.err, kDevErrBounds, e.status, e.b);
-      }
+    if (blockIdx.x == 0) report_entries<N>(p);
     int k = 0, n_q = 0, n_rope = 0, n_pair = 0;
     auto publish = [&](const Item& it) {
       if (k >= 2) wait(&ax->item_free[k & 1], ((k >> 1) + 1) & 1, 510);
@@ -369,54 +188,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       ++k;
     };
-    int v = lo < hi ? ax->found_seq : -1;
-    long long at = lo;                                       // position on the line
-    long long start = v >= 0 ? ax->found_start : 0;          // of gang g of entry v
-    Entry e;
-    int g = 0;
-    if (v >= 0) e = entry_at<N>(p, v);
-    while (ok && v >= 0 && at < hi) {
-      const int nt = gang_tiles<N>(p, e, g);
-      const long long next = start + nt + kItemCost;
-      if (at >= next) {                                      // this share begins behind gang g
-        start = next;
-        if (++g >= e.gangs) {
-          g = 0;
-          do ++v;
-          while (v < n_entries && (e = entry_at<N>(p, v)).gangs == 0);
-          if (v >= n_entries) break;
-        }
-        continue;
-      }
-      const int t0 = static_cast<int>(min(at - start, static_cast<long long>(nt)));
-      const int t1 = static_cast<int>(min(hi - start, static_cast<long long>(nt)));
-      const bool begins = at == start;
-      at = min(hi, next);
-      if (!begins && t0 == t1) continue;                     // only the item's constant cost is left
-      const int first = (g * p.gang + member) * N;           // row tile of this member
-      if (first >= e.rows) continue;
-      Item it;
-      it.rows = min(N, e.rows - first);
-      it.row0 = e.row0 + first;
-      it.seq_row0 = e.row0;
-      it.base = e.kv - e.q_len;
-      it.lo = e.lo;
-      it.prefix = e.prefix ? 1 : 0;
-      it.begins = begins ? 1 : 0;
-      it.pieces = 0;
-      it.last = -1;
-      it.tile0 = e.lo / kKeys + t0;
-      it.n_tiles = 0;
-      it.slot = -1;
-      if (e.status == 0) {
-        it.last = last_seen(p, e, first + it.rows);
-        const int own = it.last / kKeys + 1 - e.lo / kKeys;  // this row tile may end before the gang's last
-        it.n_tiles = max(0, min(t1, own) - t0);
-        const long long x = start + nt;                      // one past the item's last tile
-        const int g_last = static_cast<int>((x * n_groups - 1) / total);
-        it.pieces = begins ? g_last - group + 1 : 0;
-        if (!begins || t1 < nt) it.slot = static_cast<int>(blockIdx.x) * 2 + (begins ? 1 : 0);
-      }
+    Walk<N> walk(p, share, static_cast<int>(blockIdx.x));
+    Item it;
+    while (ok && walk.next(it)) {
       publish(it);
       if (!ok || it.n_tiles == 0) continue;
       if (n_q > 0) wait(&ax->q_free, (n_q - 1) & 1, 511);
@@ -427,13 +201,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c = 0; c < 9; ++c) tma_load_2d(sm + C::OFF_Q + c * N * 128, &map_q, &ax->q_full, c * 64, it.row0);
       }
       __syncwarp();
-      const int64_t kstart = seq_start(p.pt, p.kv_start, e.b);
+      const int64_t kstart = seq_start(p.pt, p.kv_start, walk.e.b);
       int my_row = 0;
       for (int i = 0; ok && i < it.n_tiles; ++i) {
         if ((i & 31) == 0) {            // cache rows of the next 32 tiles, one per lane (a tile lies in one page)
           const int t = min(i + static_cast<int>(lane), it.n_tiles - 1);
-          const int64_t r = cache_row(p.pt, e.b, kstart, (it.tile0 + t) * kKeys);
-          if (r < 0) report_error(p.err, kDevErrBounds, 504, e.b);
+          const int64_t r = cache_row(p.pt, walk.e.b, kstart, (it.tile0 + t) * kKeys);
+          if (r < 0) report_error(p.err, kDevErrBounds, 504, walk.e.b);
           my_row = r < 0 ? -1 : static_cast<int>(r);
         }
         int row = __shfl_sync(0xffffffffu, my_row, i & 31);
@@ -717,19 +491,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float v = (ax->mx[0][n] + ax->mx[1][n]) + (ax->mx[2][n] + ax->mx[3][n]);
           ax->fac[n] = v == 0.f ? 0.f : 1.f / v;
           const float lse2 = v == 0.f ? NEG_INF : mr[c] + log2f(v);      // log2 of the sum of exponentials
-          if (n < it.rows) {
-            const int r = it.row0 + n;
-            if (it.slot >= 0) {
-              p.part_lse[static_cast<int64_t>(it.slot) * N + n] = lse2;
-            } else if (p.shared) {
-              p.row_lse[static_cast<int64_t>(it.prefix ? 0 : 1) * p.total_q * H + r] = lse2;
-            } else if (p.lse != nullptr) {
-              p.lse[r] = lse2 * kLn2;
-            }
-            if (it.begins)
-              p.rec[static_cast<int64_t>(p.shared && !it.prefix ? 1 : 0) * p.total_q * H + r] =
-                  make_int4(it.slot, it.pieces, n, p.gang);
-          }
+          if (n < it.rows) store_lse(p, it, N, n, lse2);
         }
       }
       soft_sync();
@@ -739,12 +501,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
       }
       const int d0 = qd * 32 + static_cast<int>(lane);
-      float* dst32 = nullptr;
-      if (it.slot >= 0) {
-        dst32 = p.part_o + static_cast<int64_t>(it.slot) * N * 512;
-      } else if (p.shared) {
-        dst32 = p.row_o + (static_cast<int64_t>(it.prefix ? 0 : 1) * p.total_q * H + it.row0) * 512;
-      }
+      float* dst32 = fp32_rows(p, it, N);
 #pragma unroll 1
       for (int c = 0; c < 4 * N; c += 16) {
         uint32_t o[16];
@@ -895,8 +652,8 @@ DensePlan dense_plan(const dsa_batch_t* b, int n_heads, bool shared) {
   // Rows an item can hold: the rows of one sequence, or with a shared prefix
   // of the whole batch.
   const int64_t rows = static_cast<int64_t>(shared ? b->total_q : b->max_q_per_seq) * n_heads;
-  d.n = rows <= 16 ? 16 : (rows <= 32 ? 32 : 64);
-  // CTAs that share a key range: the row tiles of an average sequence, in equal
+  d.n = rows <= 16 ? 16 : (rows <= 32 ? 32 : 128);
+  // Units that share a key range: the row tiles of an average sequence, in equal
   // gangs of at most 16.
   const int64_t tiles = (static_cast<int64_t>(b->total_q) * n_heads + static_cast<int64_t>(b->num_seqs) * d.n - 1) /
                         (static_cast<int64_t>(b->num_seqs) * d.n);
@@ -907,19 +664,19 @@ DensePlan dense_plan(const dsa_batch_t* b, int n_heads, bool shared) {
 
 cudaError_t launch_dense_mla(const DenseMlaParams& p, const DensePlan& d, const CUtensorMap& map_q,
                              const CUtensorMap& map_c, cudaStream_t stream) {
-  int sms = sm_count();
-  if (sms < 1 || sms > kDenseMaxCtas) sms = kDenseMaxCtas;
-  const int ctas = sms / d.gang * d.gang;
   cudaError_t e;
-  switch (d.n) {
-    case 16: e = launch<16>(p, map_q, map_c, ctas, stream); break;
-    case 32: e = launch<32>(p, map_q, map_c, ctas, stream); break;
-    default: e = launch<64>(p, map_q, map_c, ctas, stream); break;
+  if (d.n == 128) {
+    e = launch_dense_pair(p, map_q, map_c, stream);
+  } else {
+    int ctas = sm_count();
+    if (ctas < 1 || ctas > kDenseMaxCtas) ctas = kDenseMaxCtas;
+    ctas = ctas / p.gang * p.gang;
+    e = d.n == 16 ? launch<16>(p, map_q, map_c, ctas, stream) : launch<32>(p, map_q, map_c, ctas, stream);
   }
   if (e != cudaSuccess) return e;
   const int64_t rows = static_cast<int64_t>(p.total_q) * p.n_heads;
   const int grid = static_cast<int>(rows < 148 * 16 ? rows : 148 * 16);
-  dense_merge_kernel<<<grid, 128, 0, stream>>>(p, d.n, 2 * kDenseMaxCtas);
+  dense_merge_kernel<<<grid, 128, 0, stream>>>(p, d.n, dense_slots(d.n));
   return cudaGetLastError();
 }
 

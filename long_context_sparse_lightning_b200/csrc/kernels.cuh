@@ -222,25 +222,33 @@ struct DenseMlaParams {
   uint16_t* out = nullptr;            // bf16 [total_q, H, 512]
   float* lse = nullptr;               // [total_q, H] or nullptr
   int4* rec = nullptr;                // [1 + shared, total_q * H]: partial slot (-1: none), pieces, row in it, gang
-  float* part_lse = nullptr;          // [2 * kDenseMaxCtas, N] log2 units
-  float* part_o = nullptr;            // [2 * kDenseMaxCtas, N, 512] normalised
+  float* part_lse = nullptr;          // [dense_slots(N), N] log2 units
+  float* part_o = nullptr;            // [dense_slots(N), N, 512] normalised
   float* row_lse = nullptr;           // shared: [2, total_q * H] of whole items, log2 units
   float* row_o = nullptr;             // shared: [2, total_q * H, 512]
   uint32_t* err = nullptr;
   long long budget = 2000000000LL;
 };
 constexpr int kDenseMaxCtas = 148;
-// Query rows per item (16, 32 or 64) and CTAs per gang for a batch.
+// Partial slots: two per unit (a CTA, or a CTA pair for N = 128).
+inline int dense_slots(int n) { return n == 128 ? kDenseMaxCtas : 2 * kDenseMaxCtas; }
+// Query rows per item (16, 32: one CTA; 128: a CTA pair) and units per gang for a batch.
 struct DensePlan {
   int n;
   int gang;
 };
 DensePlan dense_plan(const dsa_batch_t* b, int n_heads, bool shared);
 // The attention and the merge of its split items.  map_q: q as [total_q * H, 576],
-// box [N rows x 64]; map_c: the cache [total_keys, 576], box [64 rows x 64]; both
-// 128-byte swizzle.
+// box [dense_q_box(N) rows x 64]; map_c: the cache [total_keys, 576], box
+// [dense_c_box(N) rows x 64]; both 128-byte swizzle.
+inline uint32_t dense_q_box(int n) { return n == 128 ? 64u : static_cast<uint32_t>(n); }
+inline uint32_t dense_c_box(int n) { return n == 128 ? 32u : 64u; }
 cudaError_t launch_dense_mla(const DenseMlaParams& p, const DensePlan& d, const CUtensorMap& map_q,
                              const CUtensorMap& map_c, cudaStream_t stream);
+
+// its CTA-pair kernel (N = 128)
+cudaError_t launch_dense_pair(const DenseMlaParams& p, const CUtensorMap& map_q, const CUtensorMap& map_c,
+                              cudaStream_t stream);
 
 // ----------------------------------------------------------- expanded MLA --
 struct ExpandedMlaParams {
