@@ -150,13 +150,40 @@ def _ptr(t: Optional[torch.Tensor]):
         return None
     if not t.is_contiguous():
         raise ValueError("tensors must be contiguous")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
 def _stream(stream=None):
     if stream is None:
         stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+    return stream.cuda_stream
+
+
+# the current stream's handle of a device without building a Stream object
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _launch(fn, where, device, stream, *args):
+    """fn(*args, stream) on device number `device`, on its current stream unless one is given."""
+    if device < 0:
+        raise ValueError(f"{where}: tensors on a CUDA device")
+    handle = _raw_stream(device) if stream is None else stream.cuda_stream
+    if device == torch.cuda.current_device():
+        status = fn(*args, handle)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, handle)
+    if status != 0:
+        raise DSAError(status, where)
+
+
+def _one_device(where, first, *others):
+    device = first.get_device()
+    for t in others:
+        if t is not None and t.get_device() != device:
+            raise ValueError(f"{where}: tensors on one device")
+    return device
 
 
 def _check(status: int, where: str):
@@ -276,13 +303,12 @@ def forward(batch: Batch, q_fp8, q_scale, w, k_fp8, k_scale, k_sel: int, q, kv, 
 
 
 def _check_mla(where, batch, q, q_dim, out, out_dim, lse):
-    n_heads = q.shape[1] if q.dim() == 3 else 0
-    if q.dtype != torch.bfloat16 or tuple(q.shape) != (batch.total_q, n_heads, q_dim) or out.dtype != torch.bfloat16 \
-            or tuple(out.shape) != (batch.total_q, n_heads, out_dim) \
-            or (lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (batch.total_q, n_heads))):
+    n, h = batch.total_q, q.shape[1] if q.dim() == 3 else 0
+    if q.dtype != torch.bfloat16 or q.shape != (n, h, q_dim) or out.dtype != torch.bfloat16 \
+            or out.shape != (n, h, out_dim) or (lse is not None and (lse.dtype != torch.float32 or lse.shape != (n, h))):
         raise ValueError(f"{where}: q bf16 [total_q, heads, {q_dim}], out bf16 [total_q, heads, {out_dim}], "
                          "lse fp32 [total_q, heads] or None")
-    return int(n_heads)
+    return h
 
 
 def _check_cache(where, batch, kv):
@@ -295,8 +321,9 @@ def dense_mla(batch: Batch, q, kv, sm_scale: float, out, lse, ws, stream=None):
     kv [total_keys, 576] -> out [total_q, heads, 512], lse (natural log) or None; ws of OP_DENSE_MLA."""
     n_heads = _check_mla("dense_mla", batch, q, LATENT_DIM, out, VALUE_DIM, lse)
     _check_cache("dense_mla", batch, kv)
-    _check(_lib().dsa_dense_mla(batch.ref, _ptr(q), n_heads, _ptr(kv), float(sm_scale), _ptr(out), _ptr(lse),
-                                _ptr(ws), ws.numel(), _stream(stream)), "dsa_dense_mla")
+    dev = _one_device("dense_mla", q, kv, out, lse, ws, batch.cu_q)
+    _launch(_lib().dsa_dense_mla, "dsa_dense_mla", dev, stream, batch.ref, _ptr(q), n_heads, _ptr(kv), sm_scale,
+            _ptr(out), _ptr(lse), _ptr(ws), ws.numel())
 
 
 def prefix_mla(batch: Batch, prefix_len: int, q, kv, sm_scale: float, out, lse, ws, stream=None):
@@ -304,8 +331,9 @@ def prefix_mla(batch: Batch, prefix_len: int, q, kv, sm_scale: float, out, lse, 
     row 0), which are read and multiplied once for all; ws of OP_PREFIX_MLA."""
     n_heads = _check_mla("prefix_mla", batch, q, LATENT_DIM, out, VALUE_DIM, lse)
     _check_cache("prefix_mla", batch, kv)
-    _check(_lib().dsa_prefix_mla(batch.ref, int(prefix_len), _ptr(q), n_heads, _ptr(kv), float(sm_scale), _ptr(out),
-                                 _ptr(lse), _ptr(ws), ws.numel(), _stream(stream)), "dsa_prefix_mla")
+    dev = _one_device("prefix_mla", q, kv, out, lse, ws, batch.cu_q)
+    _launch(_lib().dsa_prefix_mla, "dsa_prefix_mla", dev, stream, batch.ref, prefix_len, _ptr(q), n_heads, _ptr(kv),
+            sm_scale, _ptr(out), _ptr(lse), _ptr(ws), ws.numel())
 
 
 def expanded_mla(batch: Batch, q, kv_up, rope, sm_scale: float, out, lse, ws, stream=None):
@@ -313,15 +341,16 @@ def expanded_mla(batch: Batch, q, kv_up, rope, sm_scale: float, out, lse, ws, st
     128 value dims), rope [total_keys, 64] (rows may lie apart, e.g. latent[:, 512:]) -> out [total_q, heads, 128],
     lse or None; flat caches; ws of OP_EXPANDED_MLA."""
     n_heads = _check_mla("expanded_mla", batch, q, 192, out, 128, lse)
-    if kv_up.dtype != torch.bfloat16 or kv_up.dim() != 3 or tuple(kv_up.shape[1:]) != (n_heads, 256) \
-            or kv_up.shape[0] < batch.c.total_keys or rope.dtype != torch.bfloat16 or rope.dim() != 2 \
-            or rope.shape[1] != 64 or rope.shape[0] < batch.c.total_keys or rope.stride(1) != 1:
+    keys = batch.c.total_keys
+    if kv_up.dtype != torch.bfloat16 or kv_up.dim() != 3 or kv_up.shape[1:] != (n_heads, 256) \
+            or kv_up.shape[0] < keys or rope.dtype != torch.bfloat16 or rope.dim() != 2 \
+            or rope.shape[1] != 64 or rope.shape[0] < keys or rope.stride(1) != 1:
         raise ValueError("expanded_mla: kv_up bf16 [total_keys, heads, 256], rope bf16 [total_keys, 64]")
     # a single row has no stride of its own
-    stride = int(rope.stride(0)) if rope.shape[0] > 1 else max(64, int(rope.stride(0)) // 8 * 8)
-    _check(_lib().dsa_expanded_mla(batch.ref, _ptr(q), n_heads, _ptr(kv_up), ctypes.c_void_p(rope.data_ptr()), stride,
-                                   float(sm_scale), _ptr(out), _ptr(lse), _ptr(ws), ws.numel(), _stream(stream)),
-           "dsa_expanded_mla")
+    stride = rope.stride(0) if rope.shape[0] > 1 else 64
+    dev = _one_device("expanded_mla", q, kv_up, rope, out, lse, ws, batch.cu_q)
+    _launch(_lib().dsa_expanded_mla, "dsa_expanded_mla", dev, stream, batch.ref, _ptr(q), n_heads, _ptr(kv_up),
+            rope.data_ptr(), stride, sm_scale, _ptr(out), _ptr(lse), _ptr(ws), ws.numel())
 
 
 def page_tables(q_len, kv_before, free_pages, page_size: int, block_table, cu_q, kv_len, pos, slots, pages_used, ws,
@@ -329,17 +358,20 @@ def page_tables(q_len, kv_before, free_pages, page_size: int, block_table, cu_q,
     """Block tables, offsets, positions and cache slots of a step's new tokens from the requests' lengths:
     q_len, kv_before int32 [B], free_pages int32 -> block_table int32 [B, blocks] (new pages written behind the
     held ones), cu_q int32 [B + 1], kv_len int32 [B], pos int32 and slots int64 [max_tokens], pages_used int32 [1]."""
-    n, i32 = q_len.numel(), torch.int32
-    if any(t.dtype != i32 for t in (q_len, kv_before, free_pages, block_table, cu_q, kv_len, pos, pages_used)) \
-            or slots.dtype != torch.int64 or kv_before.numel() != n or block_table.dim() != 2 \
-            or block_table.shape[0] != n or cu_q.numel() != n + 1 or kv_len.numel() != n \
-            or slots.numel() != pos.numel() or pages_used.numel() != 1:
+    n, tokens, i32, dev = q_len.numel(), pos.numel(), torch.int32, q_len.get_device()
+    for t in (q_len, kv_before, free_pages, block_table, cu_q, kv_len, pos, pages_used):
+        if t.dtype is not i32 or t.get_device() != dev or not t.is_contiguous():
+            raise ValueError("page_tables: contiguous int32 tensors on one device (int64 slots)")
+    blocks = block_table.shape[1] if block_table.dim() == 2 else 0
+    if slots.dtype is not torch.int64 or slots.get_device() != dev or not slots.is_contiguous() \
+            or ws.get_device() != dev or kv_before.numel() != n or block_table.numel() != n * blocks \
+            or cu_q.numel() != n + 1 or kv_len.numel() != n or slots.numel() != tokens or pages_used.numel() != 1:
         raise ValueError("page_tables: int32 q_len, kv_before, kv_len [B], cu_q [B + 1], block_table [B, blocks], "
                          "free_pages, pos [max_tokens], pages_used [1]; int64 slots [max_tokens]")
-    _check(_lib().dsa_page_tables(n, _ptr(q_len), _ptr(kv_before), _ptr(free_pages), free_pages.numel(),
-                                  int(page_size), _ptr(block_table), int(block_table.shape[1]), pos.numel(),
-                                  _ptr(cu_q), _ptr(kv_len), _ptr(pos), _ptr(slots), _ptr(pages_used), _ptr(ws),
-                                  ws.numel(), _stream(stream)), "dsa_page_tables")
+    _launch(_lib().dsa_page_tables, "dsa_page_tables", dev, stream, n, q_len.data_ptr(), kv_before.data_ptr(),
+            free_pages.data_ptr(), free_pages.numel(), page_size, block_table.data_ptr(), blocks, tokens,
+            cu_q.data_ptr(), kv_len.data_ptr(), pos.data_ptr(), slots.data_ptr(), pages_used.data_ptr(), ws.data_ptr(),
+            ws.numel())
 
 
 def quantize_fp8(x, codes, scales, stream=None):

@@ -67,6 +67,7 @@ dsa_status_t run_dense(const dsa_batch_t* b, int prefix_len, const void* q, int 
   p.shared = shared ? 1 : 0;
   p.prefix_len = shared ? prefix_len : 0;
   p.scale_log2 = static_cast<float>(static_cast<double>(sm_scale) * 1.4426950408889634);
+  p.kv = static_cast<const uint16_t*>(kv);
   p.out = static_cast<uint16_t*>(out);
   p.lse = lse;
   p.rec = reinterpret_cast<int4*>(base + l.rec);

@@ -15,7 +15,10 @@ namespace dense {
 
 constexpr int kTile = 64;                 // keys per tile
 constexpr float kGrow = 24.f;             // log2 units a score may exceed its row's reference by
-constexpr int kItemCost = 2;              // an item's prologue and epilogue, in tiles
+// An item's prologue and epilogue in tiles: ~3 us of 1.7 us in the one-CTA
+// kernel, ~5 us of 0.8 us in the pair kernel.
+template <int N>
+constexpr int kItemCost = N == 128 ? 6 : 2;
 constexpr int kMinShare = 2;              // tiles (and item costs) a gang takes at least
 constexpr float kLn2 = 0.69314718055994531f;
 
@@ -45,20 +48,22 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// The softmax warps' barrier; returns the OR of `v` over them.
-__device__ __forceinline__ bool soft_any(bool v) {
+// Barrier `id` of `threads` threads; the first returns the OR of `v` over them.
+__device__ __forceinline__ bool bar_any(bool v, uint32_t id, uint32_t threads) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.u32 p, %1, 0;\n\t"
-      "barrier.cta.red.or.pred q, 1, 128, p;\n\t"
+      "barrier.cta.red.or.pred q, %2, %3, p;\n\t"
       "selp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
-      : "r"(v ? 1u : 0u)
+      : "r"(v ? 1u : 0u), "r"(id), "r"(threads)
       : "memory");
   return r != 0;
 }
-__device__ __forceinline__ void soft_sync() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ void bar_sync(uint32_t id, uint32_t threads) {
+  asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
 
 // Non-finite bf16 values become 0 (both halves of a word).
 __device__ __forceinline__ uint32_t finite_or_zero(uint32_t w) {
@@ -78,36 +83,55 @@ struct Entry {
   int gangs;           // groups of W row tiles
   int status;          // 0, or the error site
   bool prefix;
+  int64_t kstart;      // flat caches: row of position 0
 };
 
+// What an entry is made of, read at once.
+struct RawEntry {
+  int q0, q1, kv;
+  int64_t kstart;
+};
+
+__device__ __forceinline__ RawEntry read_entry(const DenseMlaParams& p, int v) {
+  RawEntry w{0, 0, 0, 0};
+  if (v >= p.num_seqs + p.shared) return w;
+  if (p.shared && v == 0) {
+    w.q1 = __ldg(&p.cu_q[p.num_seqs]);
+    return w;
+  }
+  const int b = v - p.shared;
+  w.q0 = __ldg(&p.cu_q[b]);
+  w.q1 = __ldg(&p.cu_q[b + 1]);
+  w.kv = __ldg(&p.kv_len[b]);
+  w.kstart = seq_start(p.pt, p.kv_start, b);
+  return w;
+}
+
 template <int N>
-__device__ __forceinline__ Entry entry_at(const DenseMlaParams& p, int v) {
+__device__ __forceinline__ Entry make_entry(const DenseMlaParams& p, int v, const RawEntry& w) {
   Entry e;
   e.status = 0;
   e.prefix = p.shared && v == 0;
-  const int b = p.shared ? v - 1 : v;
+  e.kstart = w.kstart;
   if (e.prefix) {
-    const int n = min(max(__ldg(&p.cu_q[p.num_seqs]), 0), p.total_q);
-    e.row0 = 0;
-    e.rows = p.prefix_len > 0 ? n * p.n_heads : 0;
-    e.q_len = n;
-    e.kv = p.prefix_len;
     e.b = 0;
+    e.row0 = 0;
+    e.q_len = min(max(w.q1, 0), p.total_q);
+    e.rows = p.prefix_len > 0 ? e.q_len * p.n_heads : 0;
+    e.kv = p.prefix_len;
     e.lo = 0;
   } else {
-    const int q0 = __ldg(&p.cu_q[b]), q1 = __ldg(&p.cu_q[b + 1]);
-    e.b = b;
-    e.kv = __ldg(&p.kv_len[b]);
+    e.b = v - p.shared;
+    e.kv = w.kv;
     e.lo = p.shared ? p.prefix_len : 0;
-    if (q0 < 0 || q1 < q0 || q1 > p.total_q || (b == 0 && q0 != 0)) {   // no rows of q: nothing is read or written
-      e.row0 = e.rows = e.q_len = 0;
+    if (w.q0 < 0 || w.q1 < w.q0 || w.q1 > p.total_q || (e.b == 0 && w.q0 != 0)) {
+      e.row0 = e.rows = e.q_len = 0;                // no rows of q: nothing is read or written
       e.status = 501;
     } else {
-      e.row0 = q0 * p.n_heads;
-      e.q_len = q1 - q0;
+      e.row0 = w.q0 * p.n_heads;
+      e.q_len = w.q1 - w.q0;
       e.rows = e.q_len * p.n_heads;
-      const int64_t ks = seq_start(p.pt, p.kv_start, b);
-      if (e.q_len > e.kv || e.kv > p.max_kv_len || !seq_rows_ok(p.pt, ks, e.kv, p.total_keys))
+      if (e.q_len > e.kv || e.kv > p.max_kv_len || !seq_rows_ok(p.pt, w.kstart, e.kv, p.total_keys))
         e.status = 502;
       else if (e.q_len > 0 && e.kv - e.q_len < e.lo)
         e.status = 503;                             // the sequence does not hold the whole prefix
@@ -115,6 +139,11 @@ __device__ __forceinline__ Entry entry_at(const DenseMlaParams& p, int v) {
   }
   e.gangs = (e.rows + N * p.gang - 1) / (N * p.gang);
   return e;
+}
+
+template <int N>
+__device__ __forceinline__ Entry entry_at(const DenseMlaParams& p, int v) {
+  return make_entry<N>(p, v, read_entry(p, v));
 }
 
 // Last position the rows [.., row_end) of the entry see.
@@ -132,57 +161,94 @@ __device__ __forceinline__ int gang_tiles(const DenseMlaParams& p, const Entry& 
 }
 
 template <int N>
-__device__ __forceinline__ long long entry_cost(const DenseMlaParams& p, int v) {
-  const Entry e = entry_at<N>(p, v);
+__device__ __forceinline__ long long entry_cost(const DenseMlaParams& p, const Entry& e) {
   if (e.prefix || e.gangs <= 1 || e.status != 0)
-    return e.gangs > 0 ? static_cast<long long>(e.gangs) * (gang_tiles<N>(p, e, 0) + kItemCost) : 0;
+    return e.gangs > 0 ? static_cast<long long>(e.gangs) * (gang_tiles<N>(p, e, 0) + kItemCost<N>) : 0;
   long long c = 0;
-  for (int g = 0; g < e.gangs; ++g) c += gang_tiles<N>(p, e, g) + kItemCost;
+  for (int g = 0; g < e.gangs; ++g) c += gang_tiles<N>(p, e, g) + kItemCost<N>;
   return c;
 }
 
-// One gang's share [lo, hi) of the line of `total`, and where it begins.
+// One gang's share [lo, hi) of the line, and where it begins.  The first `rem` of
+// the gangs take per + 1 units of cost, the others per.
 struct Share {
-  long long total, lo, hi, start;      // start: of entry `entry` on the line
-  int entry, gang, gangs, member;
+  long long per, lo, hi, start;        // start: of entry `entry` on the line
+  int rem, entry, gang, gangs, member;
+  Entry e;                             // entry `entry`
 };
+
+// a / b for a >= 0, b > 0 (a 64-bit division costs several hundred cycles)
+__device__ __forceinline__ long long divide(long long a, long long b) {
+  if (((a | b) >> 31) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
+
+// The gang whose share holds position x of the line.
+__device__ __forceinline__ int gang_of(const Share& s, long long x) {
+  const long long wide = s.rem * (s.per + 1);
+  return static_cast<int>(x < wide ? divide(x, s.per + 1) : s.rem + divide(x - wide, s.per));
+}
 
 // Shared memory of find_share.
 struct ShareScratch {
-  long long scan[8];
+  long long scan[16];
   long long start;
   int32_t entry;
+  Entry e;
 };
 
-// Called by every thread of the block (THREADS <= 256); unit of n_units.
+// Called by every thread of the block (THREADS <= 512); unit of n_units.  The
+// lengths are read once where the block has a thread per entry.  Entries that are
+// out of range go to the error word, once per launch.
+// `first` is read_entry of entry threadIdx.x, read before the block's other preparations.
 template <int N, int THREADS>
-__device__ __forceinline__ Share find_share(const DenseMlaParams& p, ShareScratch& sc, int unit, int n_units) {
+__device__ __forceinline__ Share find_share(const DenseMlaParams& p, ShareScratch& sc, const RawEntry& first, int unit,
+                                            int n_units) {
   constexpr int WARPS = THREADS / 32;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int n_entries = p.num_seqs + (p.shared ? 1 : 0);
-  long long mine = 0;
-  for (int v = tid; v < n_entries; v += THREADS) mine += entry_cost<N>(p, v);
+  long long mine = 0, cost0 = 0;
+  Entry e0{};
+  for (int v = tid; v < n_entries; v += THREADS) {
+    const Entry e = v == tid ? make_entry<N>(p, v, first) : entry_at<N>(p, v);
+    const long long c = entry_cost<N>(p, e);
+    if (blockIdx.x == 0 && e.status != 0) report_error(p.err, kDevErrBounds, e.status, e.b);
+    mine += c;
+    if (v == tid) {
+      e0 = e;
+      cost0 = c;
+    }
+  }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
   if (lane == 0) sc.scan[warp] = mine;
   if (tid == 0) sc.entry = -1;
   __syncthreads();
   Share s;
-  s.total = 0;
+  long long total = 0;
 #pragma unroll
-  for (int w = 0; w < WARPS; ++w) s.total += sc.scan[w];
+  for (int w = 0; w < WARPS; ++w) total += sc.scan[w];
   s.gang = unit / p.gang;
-  s.member = unit % p.gang;
+  s.member = unit - s.gang * p.gang;
   s.gangs = static_cast<int>(
-      min(static_cast<long long>(n_units / p.gang), max(1LL, (s.total + kMinShare - 1) / kMinShare)));
-  s.lo = s.gang < s.gangs ? s.total * s.gang / s.gangs : s.total;
-  s.hi = s.gang < s.gangs ? s.total * (s.gang + 1) / s.gangs : s.total;
+      min(static_cast<long long>(n_units / p.gang), max(1LL, (total + kMinShare - 1) / kMinShare)));
+  s.per = divide(total, s.gangs);
+  s.rem = static_cast<int>(total - s.per * s.gangs);
+  s.lo = s.gang < s.gangs ? s.gang * s.per + min(s.gang, s.rem) : total;
+  s.hi = s.gang < s.gangs ? s.lo + s.per + (s.gang < s.rem ? 1 : 0) : total;
   __syncthreads();
   if (s.lo < s.hi) {
     long long base = 0;
     for (int v0 = 0; v0 < n_entries; v0 += THREADS) {
       const int v = v0 + tid;
-      const long long c = v < n_entries ? entry_cost<N>(p, v) : 0;
+      long long c = cost0;
+      if (v0 > 0) {
+        c = 0;
+        if (v < n_entries) {
+          e0 = entry_at<N>(p, v);
+          c = entry_cost<N>(p, e0);
+        }
+      }
       long long inc = c;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -201,6 +267,7 @@ __device__ __forceinline__ Share find_share(const DenseMlaParams& p, ShareScratc
       if (c > 0 && start <= s.lo && s.lo < start + c) {
         sc.entry = v;
         sc.start = start;
+        sc.e = e0;
       }
       base += all;
       __syncthreads();
@@ -209,6 +276,7 @@ __device__ __forceinline__ Share find_share(const DenseMlaParams& p, ShareScratc
   }
   s.entry = s.lo < s.hi ? sc.entry : -1;
   s.start = s.entry >= 0 ? sc.start : 0;
+  s.e = sc.e;
   return s;
 }
 
@@ -222,16 +290,14 @@ struct Walk {
   Entry e;
 
   __device__ __forceinline__ Walk(const DenseMlaParams& p_, const Share& s, int unit_)
-      : p(p_), sh(s), unit(unit_), v(s.entry), at(s.lo), start(s.start) {
-    if (v >= 0) e = entry_at<N>(p, v);
-  }
+      : p(p_), sh(s), unit(unit_), v(s.entry), at(s.lo), start(s.start), e(s.e) {}
 
   // The next piece; false at the end of the share.
   __device__ __forceinline__ bool next(Item& it) {
     const int n_entries = p.num_seqs + (p.shared ? 1 : 0);
     while (v >= 0 && v < n_entries && at < sh.hi) {
       const int nt = gang_tiles<N>(p, e, g);
-      const long long end = start + nt + kItemCost;
+      const long long end = start + nt + kItemCost<N>;
       if (at >= end) {                                       // gang g lies before the share's position
         start = end;
         if (++g >= e.gangs) {
@@ -265,8 +331,7 @@ struct Walk {
         const int own = it.last / kTile + 1 - e.lo / kTile;  // this row tile may end before the gang's last
         it.n_tiles = max(0, min(t1, own) - t0);
         const long long x = start + nt;                      // one past the item's last tile
-        const int g_last = static_cast<int>((x * sh.gangs - 1) / sh.total);
-        it.pieces = begins ? g_last - sh.gang + 1 : 0;
+        it.pieces = begins ? gang_of(sh, x - 1) - sh.gang + 1 : 0;
         if (!begins || t1 < nt) it.slot = unit * 2 + (begins ? 1 : 0);
       }
       return true;
@@ -274,16 +339,6 @@ struct Walk {
     return false;
   }
 };
-
-// Sequences that are out of range into the error word (one warp).
-template <int N>
-__device__ __forceinline__ void report_entries(const DenseMlaParams& p) {
-  const int n_entries = p.num_seqs + (p.shared ? 1 : 0);
-  for (int v = static_cast<int>(threadIdx.x & 31u); v < n_entries; v += 32) {
-    const Entry e = entry_at<N>(p, v);
-    if (e.status != 0) report_error(p.err, kDevErrBounds, e.status, e.b);
-  }
-}
 
 // Where row n of an item's log-sum-exp (log2 units) goes, and the item's record.
 __device__ __forceinline__ void store_lse(const DenseMlaParams& p, const Item& it, int N, int n, float lse2) {

@@ -27,8 +27,8 @@
 // buffers of 32 columns.
 //
 // Roles per CTA: warp 0 items and TMA of the keys, warp 1 MMAs (rank 0), warp 2
-// TMA of the second half, warps 4-7 softmax and epilogue (thread = one row's
-// 32 keys of a tile, or 256 of its output dims).  Row references as in the one-CTA kernel.
+// TMA of the second half, warps 4-7 and 8-11 softmax of every other tile and epilogue
+// (thread = one row's 32 keys of a tile, or 128 of its output dims).  Row references as in the one-CTA kernel.
 #include <atomic>
 
 #include "dense_mla.cuh"
@@ -39,7 +39,8 @@ namespace {
 using namespace dense;
 
 constexpr int kN = 128;                   // rows per item
-constexpr int kThreads = 256;
+constexpr int kThreads = 384;
+constexpr int kSoftThreads = 256;         // two softmax warpgroups
 constexpr int kBlk = 32 * 128;            // [32 keys x 64 dims]
 constexpr int kStage = 9 * kBlk;
 constexpr int kStages = 4;
@@ -48,8 +49,12 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t TM_S = 256;            // + 32 * buffer
 
 constexpr int OFF_Q = 0;
-constexpr int OFF_P = 9 * kQBlk;          // [64 rows x 64 keys] bf16
-constexpr int OFF_KV = OFF_P + kQBlk;
+constexpr int kSBufs = 3;
+constexpr int kPBlk = 64 * 64;            // [64 rows x 32 keys] bf16, 64-byte swizzle
+constexpr int kPrefetch = 4;              // tiles that L2 is asked for ahead of the load
+
+constexpr int OFF_P = 9 * kQBlk;          // 2 x the first half of P; the second lies in the stage's block 8
+constexpr int OFF_KV = OFF_P + 2 * kPBlk;
 constexpr int OFF_AUX = OFF_KV + kStages * kStage;
 constexpr int kSmem = OFF_AUX + 2048 + 1024;
 static_assert(kSmem <= 232448, "shared memory of one CTA");
@@ -60,8 +65,9 @@ struct Aux {
   uint64_t full[kStages], empty[kStages];   // keys landed in both CTAs (rank 0's) / tile done (both)
   uint64_t rows_set[kStages];               // this stage's cache row is known (for warp 2)
   uint64_t v_full[kStages];                 // the other CTA's keys landed here
-  uint64_t s_full[2], s_free[2];
-  uint64_t p_full;
+  uint64_t s_full[kSBufs], s_free[kSBufs];
+  uint64_t p_full[2];
+  uint64_t ref_set[2];                      // tile parity: the rows' references with the tile are known
   uint64_t o_full, o_free;
   uint64_t item_full[2], item_free[2];
   Item item[2];
@@ -69,10 +75,21 @@ struct Aux {
   uint32_t tmem;
   union {
     ShareScratch share;
-    float mx[2][64];                        // per half of a tile's keys: row maxima / row sums
+    float mx[2][2][64];                     // per warpgroup and half of a tile's keys: row maxima / row sums
   };
+  float ref[64];                            // the rows' references
 };
 static_assert(sizeof(Aux) <= 2048, "");
+
+// 32 bytes to a 16-byte aligned address.
+__device__ __forceinline__ void store_32(void* dst, const uint32_t (&v)[8]) {
+  if ((reinterpret_cast<uintptr_t>(dst) & 31u) == 0) {
+    st_global_32(dst, v);
+  } else {
+    reinterpret_cast<uint4*>(dst)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<uint4*>(dst)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+  }
+}
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     dense_pair_kernel(const DenseMlaParams p, const __grid_constant__ CUtensorMap map_q,
@@ -86,6 +103,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t warp = warp_id(), lane = lane_id();
   const int tid = threadIdx.x;
   const int H = p.n_heads;
+  const RawEntry first = read_entry(p, tid);      // in flight during the set-up
 
   if (tid == 0) {
     mbar_init(&ax->q_full, 1);
@@ -96,15 +114,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(&ax->rows_set[i], 1);
       mbar_init(&ax->v_full[i], 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kSBufs; ++i) {
       mbar_init(&ax->s_full[i], 1);
-      mbar_init(&ax->s_free[i], 8);                    // softmax warps of both CTAs
-      mbar_init(&ax->item_full[i], 1);
-      mbar_init(&ax->item_free[i], rank == 0 ? 6 : 5); // softmax warps, warp 2, rank 0's MMA thread
+      mbar_init(&ax->s_free[i], 8);                    // a softmax warpgroup of both CTAs
     }
-    mbar_init(&ax->p_full, 8);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ax->p_full[i], 8);
+      mbar_init(&ax->item_full[i], 1);
+      mbar_init(&ax->ref_set[i], 4);
+      mbar_init(&ax->item_free[i], rank == 0 ? 10 : 9); // softmax warps, warp 2, rank 0's MMA thread
+    }
     mbar_init(&ax->o_full, 1);
-    mbar_init(&ax->o_free, 8);
+    mbar_init(&ax->o_free, 16);
     fence_mbar_init();
     prefetch_tmap(&map_q);
     prefetch_tmap(&map_c);
@@ -113,7 +134,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const Share share = find_share<kN, kThreads>(p, ax->share, unit, n_units);
+  const Share share = find_share<kN, kThreads>(p, ax->share, first, unit, n_units);
   __syncthreads();
   cluster_sync();                                      // the other CTA's barriers exist
   const uint32_t tmem = ax->tmem;
@@ -128,7 +149,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       ok = __all_sync(0xffffffffu, ok);
     };
-    if (blockIdx.x == 0) report_entries<kN>(p);
     int k = 0, n_q = 0, t = 0;
     auto publish = [&](const Item& it) {
       if (k >= 2) wait(&ax->item_free[k & 1], ((k >> 1) + 1) & 1, 550);
@@ -154,16 +174,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           tma_load_2d_pair(sm + OFF_Q + c * kQBlk, &map_q, q_full, c * 64, it.row0 + 64 * static_cast<int>(rank));
       }
       __syncwarp();
-      const int64_t kstart = seq_start(p.pt, p.kv_start, walk.e.b);
-      int my_row = 0;
+      const int64_t kstart = walk.e.kstart;
+      // Cache rows of 32 tiles, one per lane (a tile lies in one page), and of the 32 after them.
+      auto tile_row = [&](int i) -> int {
+        if (i >= it.n_tiles) return -1;
+        const int64_t r = cache_row(p.pt, walk.e.b, kstart, (it.tile0 + i) * kTile);
+        if (r < 0 && rank == 0) report_error(p.err, kDevErrBounds, 504, walk.e.b);
+        return r < 0 ? -1 : static_cast<int>(r);
+      };
+      int my_row = tile_row(static_cast<int>(lane)), my_next = tile_row(32 + static_cast<int>(lane));
       for (int i = 0; ok && i < it.n_tiles; ++i, ++t) {
-        if ((i & 31) == 0) {            // cache rows of the next 32 tiles, one per lane (a tile lies in one page)
-          const int u = min(i + static_cast<int>(lane), it.n_tiles - 1);
-          const int64_t r = cache_row(p.pt, walk.e.b, kstart, (it.tile0 + u) * kTile);
-          if (r < 0 && rank == 0) report_error(p.err, kDevErrBounds, 504, walk.e.b);
-          my_row = r < 0 ? -1 : static_cast<int>(r);
+        if (i > 0 && (i & 31) == 0) {
+          my_row = my_next;
+          my_next = tile_row(i + 32 + static_cast<int>(lane));
         }
         const int row = __shfl_sync(0xffffffffu, my_row, i & 31);
+        const int ahead_a = __shfl_sync(0xffffffffu, my_row, (i + kPrefetch) & 31);
+        const int ahead_b = __shfl_sync(0xffffffffu, my_next, (i + kPrefetch) & 31);
         const int s = t % kStages;
         if (t >= kStages) wait(&ax->empty[s], ((t / kStages) + 1) & 1, 552);
         if (!ok) break;
@@ -175,6 +202,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           // a tile of a page outside the pool lies behind the cache: zeros arrive, no row is read
           const int y = row < 0 ? static_cast<int>(p.total_keys) : row + 32 * static_cast<int>(rank);
           for (int d = 0; d < 9; ++d) tma_load_2d_pair(sm + OFF_KV + s * kStage + d * kBlk, &map_c, full, d * 64, y);
+        }
+        // this CTA's keys of a later tile: 288 lines of one run of the cache, nine per lane
+        const int ahead = (i & 31) + kPrefetch < 32 ? ahead_a : ahead_b;
+        const int64_t y1 = static_cast<int64_t>(ahead) + 32 * static_cast<int>(rank);
+        if (ahead >= 0 && y1 + 32 <= p.total_keys) {
+          const uint8_t* at = reinterpret_cast<const uint8_t*>(p.kv) + y1 * 1152 + lane * 128;
+#pragma unroll
+          for (int c = 0; c < 9; ++c) asm volatile("prefetch.global.L2 [%0];" ::"l"(at + c * 4096));
         }
         __syncwarp();
       }
@@ -199,7 +234,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const uint32_t q_addr = smem_u32(sm + OFF_Q), p_addr = smem_u32(sm + OFF_P), kv_addr = smem_u32(sm + OFF_KV);
       bool ok = true;
       auto wait = [&](uint64_t* b, uint32_t parity, uint32_t site) {
-        if (ok && !mbar_wait_cluster(b, parity, p.budget)) {
+        if (ok && !mbar_wait(b, parity, p.budget)) {
           report_error(p.err, kDevErrTimeout, site, blockIdx.x);
           ok = false;
         }
@@ -207,8 +242,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       };
       int n_q = 0, t_s = 0, t_o = 0, n_o = 0;
       auto score = [&](bool last) {
-        const int s = t_s % kStages, sb = t_s & 1;
-        if (t_s >= 2 && !wait(&ax->s_free[sb], ((t_s >> 1) + 1) & 1, 561)) return;
+        const int s = t_s % kStages, sb = t_s % kSBufs;
+        if (t_s >= kSBufs && !wait(&ax->s_free[sb], ((t_s / kSBufs) + 1) & 1, 561)) return;
         if (!wait(&ax->full[s], (t_s / kStages) & 1, 562)) return;
         tc_fence_after();
 #pragma unroll
@@ -230,11 +265,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (nt == 0) continue;
         if (!wait(&ax->q_full, n_q & 1, 563)) break;
         ++n_q;
+        // scores run two tiles ahead, so that neither the softmax of a tile nor the
+        // load of its second half is waited for while there are scores to compute
         score(nt == 1);
+        if (ok && nt > 1) score(nt == 2);
         for (int i = 0; ok && i < nt; ++i) {
-          if (i + 1 < nt) score(i + 2 == nt);
+          if (i + 2 < nt) score(i + 3 == nt);
           const int s = t_o % kStages;
-          if (!ok || !wait(&ax->p_full, t_o & 1, 564)) break;       // P written, and all keys at each CTA's dims landed
+          if (!ok || !wait(&ax->p_full[t_o & 1], (t_o >> 1) & 1, 564)) break;       // P written, and all keys at each CTA's dims landed
           if (i == 0 && n_o > 0 && !wait(&ax->o_free, (n_o - 1) & 1, 565)) break;
           tc_fence_after();
 #pragma unroll
@@ -243,7 +281,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
               for (int j = 0; j < 2; ++j)
-                umma_f16_ss_pair(tmem + 128 * j, smem_desc(p_addr + (2 * g + kk) * 32, 16, 1024, kSwizzle128B),
+                umma_f16_ss_pair(tmem + 128 * j,
+                                 smem_desc((g == 0 ? p_addr + (t_o & 1) * kPBlk : kv_addr + s * kStage + 8 * kBlk) + kk * 32,
+                                           16, 512, kSwizzle64B),
                                  smem_desc(kv_addr + s * kStage + (4 * g + 2 * j) * kBlk + kk * 2048, kBlk, 1024,
                                            kSwizzle128B),
                                  idesc_o, (i | g | kk) ? 1u : 0u);
@@ -276,7 +316,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (int i = 0; ok && i < it.n_tiles; ++i, ++n_own) {
         const int s = n_own % kStages, pos0 = (it.tile0 + i) * kTile;
         wait(&ax->rows_set[s], (n_own / kStages) & 1, 571);
-        wait(&ax->s_full[n_own & 1], (n_own >> 1) & 1, 572);     // S has read the tile
+        wait(&ax->s_full[n_own % kSBufs], (n_own / kSBufs) & 1, 572);     // S has read the tile
         if (!ok) break;
         if (lane == 0) {
           const int row = ax->row[s], none = static_cast<int>(p.total_keys);
@@ -302,49 +342,53 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
   } else if (warp >= 4) {
     // ---------------------------------------------------- softmax, epilogue --
+    // The two warpgroups take turns at the tiles: one alone, a warp per scheduler,
+    // shows every latency of its chain (~1800 cycles a tile against ~1400 of MMAs).
+    // A row's reference passes from tile to tile through shared memory.
+    const int wg = static_cast<int>(warp >> 2) - 1;
     const int qd = static_cast<int>(warp & 3u);
     const uint32_t t_lane = tmem + (static_cast<uint32_t>(qd * 32) << 16);
     const int half = qd >> 1;                                      // keys 32 half .. of a tile, dims 256 half ..
     const int r = (qd & 1) * 32 + static_cast<int>(lane);          // row of this CTA
     const int n = 64 * static_cast<int>(rank) + r;                 // row of the item
-    const int st = tid - 128;
+    const int st = tid & 127;
+    const uint32_t wg_bar = 2 + wg;
     const float NEG_INF = __int_as_float(0xff800000);
     const float scale = p.scale_log2;
-    const uint32_t p_row = smem_u32(sm + OFF_P) + r * 128;
-    const uint32_t s_free0 = mapa_shared(smem_u32(&ax->s_free[0]), 0), p_full = mapa_shared(smem_u32(&ax->p_full), 0);
+    const uint32_t p_row = smem_u32(sm + (half == 0 ? OFF_P : OFF_KV + 8 * kBlk)) + r * 64;
+    const uint32_t s_free0 = mapa_shared(smem_u32(&ax->s_free[0]), 0), p_full0 = mapa_shared(smem_u32(&ax->p_full[0]), 0);
     const uint32_t o_free = mapa_shared(smem_u32(&ax->o_free), 0);
     bool ok = true;
     // Once a wait has run out nothing waits any more: the warps go on to the
     // end in step (their barriers keep matching) and the error word tells.
     auto wait = [&](uint64_t* b, uint32_t parity, uint32_t site) {
-      if (ok && !mbar_wait_cluster(b, parity, p.budget)) {
+      if (ok && !mbar_wait(b, parity, p.budget)) {
         report_error(p.err, kDevErrTimeout, site, blockIdx.x);
         ok = false;
       }
-      ok = __all_sync(0xffffffffu, ok);
+      __syncwarp();
     };
-    int t = 0, n_o = 0;
+    int t0 = 0, n_o = 0;              // tiles before this item, items with tiles
     for (int k = 0;; ++k) {
       wait(&ax->item_full[k & 1], (k >> 1) & 1, 580);
-      if (soft_any(!ok)) break;       // a warp that gave up must not leave the others at a barrier
+      if (bar_any(!ok, 1, kSoftThreads)) break;       // a warp that gave up must not leave the others at a barrier
       const Item it = ax->item[k & 1];
       __syncwarp();
       if (lane == 0) mbar_arrive(&ax->item_free[k & 1]);
       if (it.n_tiles < 0) break;
       const int min_lim = it.prefix ? it.last : it.base + (it.row0 - it.seq_row0) / H;
       const int lim = n >= it.rows ? -1 : (it.prefix ? it.last : it.base + (it.row0 + n - it.seq_row0) / H);
-      float m = NEG_INF, l = 0.f;     // the row's reference; this thread's share of its sum
-      for (int i = 0; i < it.n_tiles; ++i, ++t) {
-        const int sb = t & 1, s = t % kStages, pos0 = (it.tile0 + i) * kTile;
+      float m = NEG_INF, l = 0.f;     // reference and this thread's share of the row's sum in its units
+      for (int i = (t0 ^ wg) & 1; i < it.n_tiles; i += 2) {
+        const int t = t0 + i, sb = t % kSBufs, s = t % kStages, pos0 = (it.tile0 + i) * kTile;
         uint32_t x[32];
-        wait(&ax->s_full[sb], (t >> 1) & 1, 581);
+        wait(&ax->s_full[sb], (t / kSBufs) & 1, 581);
         tc_fence_after();
         tmem_ld32(t_lane + TM_S + 32 * sb, x);
         tmem_ld_wait();
         tc_fence_before();
         wait(&ax->rows_set[s], (t / kStages) & 1, 586);
         const bool skip = ax->row[s] < 0;
-        __syncwarp();
         if (lane == 0) mbar_arrive_remote(s_free0 + 8 * sb);
         const bool border = skip || pos0 < it.lo || pos0 + kTile - 1 > min_lim;
         if (border) {
@@ -354,40 +398,56 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (skip || pos < it.lo || pos > lim) x[j] = __float_as_uint(NEG_INF);
           }
         }
-        float mx = fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1]));
+        float m4[4];
 #pragma unroll
-        for (int j = 2; j < 32; ++j) mx = fmaxf(mx, __uint_as_float(x[j]));
-        mx *= scale;
+        for (int j = 0; j < 4; ++j) m4[j] = __uint_as_float(x[j]);
+#pragma unroll
+        for (int j = 4; j < 32; ++j) m4[j & 3] = fmaxf(m4[j & 3], __uint_as_float(x[j]));
+        const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * scale;
+        float now = NEG_INF;          // the row's reference before this tile
+        if (i > 0) {
+          wait(&ax->ref_set[(t - 1) & 1], ((t - 1) >> 1) & 1, 587);
+          now = ax->ref[r];
+        }
         // reference -inf: any finite score grows it, a masked one (NaN here) does not
-        if (soft_any(mx - m > kGrow)) {
-          ax->mx[half][r] = mx;
-          soft_sync();
-          const float top = fmaxf(ax->mx[0][r], ax->mx[1][r]);
-          const float f = top > m ? exp2_approx(m - top) : 1.f;
-          m = fmaxf(m, top);
-          l *= f;
-          if (i > 0) {
-            // O is idle once the previous tile's product is done
-            wait(&ax->empty[(t - 1) % kStages], ((t - 1) / kStages) & 1, 582);
-            tc_fence_after();
-#pragma unroll 1
-            for (int c = 0; c < 256; c += 32) {
-              uint32_t o[32];
-              tmem_ld32(t_lane + c, o);
-              tmem_ld_wait();
-              uint32_t a[16], b[16];
-#pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                a[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-                b[j] = __float_as_uint(__uint_as_float(o[16 + j]) * f);
-              }
-              tmem_st16(t_lane + c, a);
-              tmem_st16(t_lane + c + 16, b);
-            }
-            tmem_st_wait();
-            tc_fence_before();
+        const bool grow = bar_any(mx - now > kGrow, wg_bar, 128);
+        float f = 1.f;
+        if (grow) {
+          ax->mx[wg][half][r] = mx;
+          bar_sync(wg_bar, 128);
+          const float top = fmaxf(ax->mx[wg][0][r], ax->mx[wg][1][r]);
+          if (top > now) {
+            f = exp2_approx(now - top);
+            now = top;
           }
-          soft_sync();                // mx may be rewritten
+        }
+        if ((grow || i == 0) && half == 0) ax->ref[r] = now;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ax->ref_set[t & 1]);
+        if (now != m) {
+          l *= exp2_approx(m - now);
+          m = now;
+        }
+        if (grow && i > 0) {
+          // O is idle once the previous tile's product is done
+          wait(&ax->empty[(t - 1) % kStages], ((t - 1) / kStages) & 1, 582);
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < 256; c += 32) {
+            uint32_t o[32];
+            tmem_ld32(t_lane + c, o);
+            tmem_ld_wait();
+            uint32_t a[16], b[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              a[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+              b[j] = __float_as_uint(__uint_as_float(o[16 + j]) * f);
+            }
+            tmem_st16(t_lane + c, a);
+            tmem_st16(t_lane + c + 16, b);
+          }
+          tmem_st_wait();
+          tc_fence_before();
         }
         const float ref = m == NEG_INF ? 0.f : -m;
         uint32_t pk[16];
@@ -400,11 +460,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           pk[j] = pack_bf16(a, b);
         }
         l += sum;
-        // P is read by the previous tile's product until that is done
-        if (t > 0) wait(&ax->empty[(t - 1) % kStages], ((t - 1) / kStages) & 1, 583);
+        // the first half's buffer is read by the product before last until that is
+        // done; the second half takes the place of the tile's RoPE dims, which S has read
+        if (t > 1) wait(&ax->empty[(t - 2) % kStages], ((t - 2) / kStages) & 1, 583);
+        const uint32_t p_at = p_row + (half == 0 ? (t & 1) * kPBlk : s * kStage);
 #pragma unroll
         for (int u = 0; u < 4; ++u)
-          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(p_row + (((4 * half + u) ^ (r & 7)) << 4)),
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(p_at + ((u ^ ((r >> 1) & 3)) << 4)),
                        "r"(pk[4 * u]), "r"(pk[4 * u + 1]), "r"(pk[4 * u + 2]), "r"(pk[4 * u + 3])
                        : "memory");
         wait(&ax->v_full[s], (t / kStages) & 1, 584);
@@ -424,15 +486,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive_remote(p_full);
+        if (lane == 0) mbar_arrive_remote(p_full0 + 8 * (t & 1));
       }
+      t0 += it.n_tiles;
 
-      // ---- the row's sum over both halves of the keys ----
-      ax->mx[half][r] = l;
-      soft_sync();
-      const float sum = ax->mx[0][r] + ax->mx[1][r];
+      // ---- the row's sum over both halves of the keys and both warpgroups ----
+      float last = NEG_INF;
+      if (it.n_tiles > 0) {
+        wait(&ax->ref_set[(t0 - 1) & 1], ((t0 - 1) >> 1) & 1, 588);
+        last = ax->ref[r];
+        if (last != m) l *= exp2_approx(m - last);
+      }
+      bar_sync(wg_bar, 128);          // the last tile's maxima have been read
+      ax->mx[wg][half][r] = l;
+      bar_sync(1, kSoftThreads);
+      const float sum = (ax->mx[0][0][r] + ax->mx[0][1][r]) + (ax->mx[1][0][r] + ax->mx[1][1][r]);
       const float inv = sum == 0.f ? 0.f : 1.f / sum;
-      if (half == 0 && n < it.rows) store_lse(p, it, kN, n, sum == 0.f ? NEG_INF : m + log2f(sum));
+      if (wg == 0 && half == 0 && n < it.rows) store_lse(p, it, kN, n, sum == 0.f ? NEG_INF : last + log2f(sum));
       if (it.n_tiles > 0) {
         wait(&ax->o_full, n_o & 1, 585);
         ++n_o;
@@ -440,7 +510,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       float* dst32 = fp32_rows(p, it, kN);
 #pragma unroll 1
-      for (int c = 0; c < 256; c += 32) {
+      for (int c = 128 * wg; c < 128 * wg + 128; c += 32) {
         uint32_t o[32];
         if (it.n_tiles > 0) {
           tmem_ld32(t_lane + c, o);
@@ -451,20 +521,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         const int d = 256 * half + c;
         if (n < it.rows && dst32 != nullptr && it.n_tiles > 0) {    // an empty piece has lse = -inf, its output is not read
+          float* at = dst32 + static_cast<int64_t>(n) * 512 + d;
 #pragma unroll
-          for (int j = 0; j < 32; j += 4)
-            *reinterpret_cast<float4*>(dst32 + static_cast<int64_t>(n) * 512 + d + j) =
-                make_float4(__uint_as_float(o[j]) * inv, __uint_as_float(o[j + 1]) * inv,
-                            __uint_as_float(o[j + 2]) * inv, __uint_as_float(o[j + 3]) * inv);
+          for (int j = 0; j < 32; j += 8) {
+            uint32_t v[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = __float_as_uint(__uint_as_float(o[j + e]) * inv);
+            store_32(at + j, v);
+          }
         }
         if (n < it.rows && dst32 == nullptr) {
+          uint16_t* at = p.out + static_cast<int64_t>(it.row0 + n) * 512 + d;
 #pragma unroll
-          for (int j = 0; j < 32; j += 8)
-            *reinterpret_cast<uint4*>(p.out + static_cast<int64_t>(it.row0 + n) * 512 + d + j) = make_uint4(
-                pack_bf16(__uint_as_float(o[j]) * inv, __uint_as_float(o[j + 1]) * inv),
-                pack_bf16(__uint_as_float(o[j + 2]) * inv, __uint_as_float(o[j + 3]) * inv),
-                pack_bf16(__uint_as_float(o[j + 4]) * inv, __uint_as_float(o[j + 5]) * inv),
-                pack_bf16(__uint_as_float(o[j + 6]) * inv, __uint_as_float(o[j + 7]) * inv));
+          for (int j = 0; j < 32; j += 16) {
+            uint32_t v[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              v[e] = pack_bf16(__uint_as_float(o[j + 2 * e]) * inv, __uint_as_float(o[j + 2 * e + 1]) * inv);
+            store_32(at + j, v);
+          }
         }
         __syncwarp();
       }
@@ -473,7 +548,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive_remote(o_free);
       }
-      soft_sync();                    // mx may be rewritten
+      bar_sync(1, kSoftThreads);      // mx and ref may be rewritten
     }
   }
   tc_fence_before();

@@ -59,8 +59,8 @@ template <int N>
 struct Cfg {
   // Scores run one tile ahead of the second product, which holds its tile's four
   // pairs until it is done: eight pair slots at least.
-  static constexpr int ROPE_SLOTS = N == 64 ? 1 : 2;
-  static constexpr int PAIR_SLOTS = N == 64 ? 8 : (N == 32 ? 9 : 10);
+  static constexpr int ROPE_SLOTS = 2;
+  static constexpr int PAIR_SLOTS = N == 32 ? 9 : 10;
   static_assert(PAIR_SLOTS >= 8, "two tiles in flight");
   static constexpr int OFF_Q = 0;                                    // 9 blocks of [N rows x 64 dims]
   static constexpr int OFF_P = 9 * N * 128;                          // 2 x [64 keys x 64 rows] bf16
@@ -85,15 +85,15 @@ struct Aux {
   uint32_t tmem;
   union {
     ShareScratch share;
-    float mx[4][64];        // per softmax warp: row maxima / row sums
+    float mx[4][32];        // per softmax warp: row maxima / row sums
   };
-  float fac[64];            // rescaling factors, inverse row sums
-  int32_t lim[64];          // last position each row sees
+  float fac[32];            // rescaling factors, inverse row sums
+  float ref[32];            // the rows' references, at the end of an item
+  int32_t lim[32];          // last position each row sees
 };
 static_assert(sizeof(Aux) <= 2048, "");
 
 // 16 TMEM lanes x N columns, the layout of tmem_ld_16x256b_x8
-__device__ __forceinline__ void ld_scores(uint32_t t, uint32_t (&r)[32]) { tmem_ld_16x256b_x8(t, r); }
 __device__ __forceinline__ void ld_scores(uint32_t t, uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
@@ -129,6 +129,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t warp = warp_id(), lane = lane_id();
   const int tid = threadIdx.x;
   const int H = p.n_heads;
+  const RawEntry first = read_entry(p, tid);      // in flight during the set-up
 
   if (tid == 0) {
     mbar_init(&ax->q_full, 1);
@@ -163,7 +164,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const Share share = find_share<N, kThreads>(p, ax->share, static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x));
+  const Share share = find_share<N, kThreads>(p, ax->share, first, static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x));
   __syncthreads();
   const uint32_t tmem = ax->tmem;
 
@@ -177,7 +178,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       ok = __all_sync(0xffffffffu, ok);
     };
-    if (blockIdx.x == 0) report_entries<N>(p);
     int k = 0, n_q = 0, n_rope = 0, n_pair = 0;
     auto publish = [&](const Item& it) {
       if (k >= 2) wait(&ax->item_free[k & 1], ((k >> 1) + 1) & 1, 510);
@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c = 0; c < 9; ++c) tma_load_2d(sm + C::OFF_Q + c * N * 128, &map_q, &ax->q_full, c * 64, it.row0);
       }
       __syncwarp();
-      const int64_t kstart = seq_start(p.pt, p.kv_start, walk.e.b);
+      const int64_t kstart = walk.e.kstart;
       int my_row = 0;
       for (int i = 0; ok && i < it.n_tiles; ++i) {
         if ((i & 31) == 0) {            // cache rows of the next 32 tiles, one per lane (a tile lies in one page)
@@ -343,20 +343,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         report_error(p.err, kDevErrTimeout, site, blockIdx.x);
         ok = false;
       }
-      ok = __all_sync(0xffffffffu, ok);
+      __syncwarp();
     };
     int t = 0, n_o = 0;       // tiles and items so far
     for (int k = 0;; ++k) {
       wait(&ax->item_full[k & 1], (k >> 1) & 1, 530);
       // a warp that gave up must not leave the others at a barrier
-      if (soft_any(!ok)) break;
+      if (bar_any(!ok, 1, kSoftThreads)) break;
       const Item it = ax->item[k & 1];
       __syncwarp();
       if (lane == 0) mbar_arrive(&ax->item_free[k & 1]);
       if (it.n_tiles < 0) break;
       if (st < N)
         ax->lim[st] = st >= it.rows ? -1 : (it.prefix ? it.last : it.base + (it.row0 + st - it.seq_row0) / H);
-      soft_sync();
+      bar_sync(1, kSoftThreads);
       const int min_lim = ax->lim[0];       // row 0 is the earliest token's
       float mr[2 * KC], l[2 * KC];
 #pragma unroll
@@ -392,7 +392,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int e = 0; e < 4; ++e)
             // reference -inf: any finite score grows it, a masked one (NaN here) does not
             grow |= fmaf(__uint_as_float(s[4 * kc + e]), scale, -mr[2 * kc + (e & 1)]) > kGrow;
-        if (soft_any(grow)) {
+        if (bar_any(grow, 1, kSoftThreads)) {
           // new references: the tile's row maxima where they exceed the old ones
 #pragma unroll
           for (int c = 0; c < 2 * KC; ++c) {
@@ -401,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int o = 4; o <= 16; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
             if (lane < 4) ax->mx[qd][8 * (c >> 1) + col0 + (c & 1)] = m;
           }
-          soft_sync();
+          bar_sync(1, kSoftThreads);
 #pragma unroll
           for (int c = 0; c < 2 * KC; ++c) {
             const int n = 8 * (c >> 1) + col0 + (c & 1);
@@ -411,7 +411,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             l[c] *= f;
             if (qd == 0 && (lane >> 2) == 0) ax->fac[n] = f;
           }
-          soft_sync();
+          bar_sync(1, kSoftThreads);
           if (i > 0) {
             // O^T is idle once the previous tile's product is done
             wait(&ax->p_empty[(t - 1) & 1], ((t - 1) >> 1) & 1, 532);
@@ -483,18 +483,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int o = 4; o <= 16; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
         if (lane < 4) ax->mx[qd][8 * (c >> 1) + col0 + (c & 1)] = v;
       }
-      soft_sync();
+      bar_sync(1, kSoftThreads);
+      float row_sum = 0.f;               // threads 0 .. N-1: row st's
+      if (st < N) {
+        row_sum = (ax->mx[0][st] + ax->mx[1][st]) + (ax->mx[2][st] + ax->mx[3][st]);
+        ax->fac[st] = row_sum == 0.f ? 0.f : 1.f / row_sum;
+      }
+      // the row's reference lies with the threads of its column
       if (qd == 0 && lane < 4) {
 #pragma unroll
-        for (int c = 0; c < 2 * KC; ++c) {
-          const int n = 8 * (c >> 1) + col0 + (c & 1);
-          const float v = (ax->mx[0][n] + ax->mx[1][n]) + (ax->mx[2][n] + ax->mx[3][n]);
-          ax->fac[n] = v == 0.f ? 0.f : 1.f / v;
-          const float lse2 = v == 0.f ? NEG_INF : mr[c] + log2f(v);      // log2 of the sum of exponentials
-          if (n < it.rows) store_lse(p, it, N, n, lse2);
-        }
+        for (int c = 0; c < 2 * KC; ++c) ax->ref[8 * (c >> 1) + col0 + (c & 1)] = mr[c];
       }
-      soft_sync();
+      bar_sync(1, kSoftThreads);
+      if (st < it.rows) store_lse(p, it, N, st, row_sum == 0.f ? NEG_INF : ax->ref[st] + log2f(row_sum));
       if (it.n_tiles > 0) {
         wait(&ax->o_full, n_o & 1, 535);
         ++n_o;
@@ -502,35 +503,43 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const int d0 = qd * 32 + static_cast<int>(lane);
       float* dst32 = fp32_rows(p, it, N);
+      // four chunks of 16 columns at a time (the loads' latency once)
 #pragma unroll 1
-      for (int c = 0; c < 4 * N; c += 16) {
-        uint32_t o[16];
+      for (int c0 = 0; c0 < 4 * N; c0 += 64) {
+        uint32_t o[4][16];
         if (it.n_tiles > 0) {
-          ld_cols16(tmem + lane_base + c, o);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) ld_cols16(tmem + lane_base + c0 + 16 * q, o[q]);
           tmem_ld_wait();
         } else {
 #pragma unroll
-          for (int j = 0; j < 16; ++j) o[j] = 0u;
+          for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int j = 0; j < 16; ++j) o[q][j] = 0u;
         }
-        const int n0 = c % N, d = (c / N) * 128 + d0;
-        if (dst32 != nullptr) {
-          if (it.n_tiles > 0) {          // an empty piece has lse = -inf, its output is not read
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
-              if (n0 + j < it.rows)
-                dst32[static_cast<int64_t>(n0 + j) * 512 + d] = __uint_as_float(o[j]) * ax->fac[n0 + j];
-          }
-        } else {
-          // lane pairs exchange so that each stores two neighbouring dims of one row
+        for (int q = 0; q < 4; ++q) {
+          const int c = c0 + 16 * q, n0 = c % N, d = (c / N) * 128 + d0;
+          if (dst32 != nullptr) {
+            if (it.n_tiles > 0) {          // an empty piece has lse = -inf, its output is not read
 #pragma unroll
-          for (int j = 0; j < 16; j += 2) {
-            const float a = __uint_as_float(o[j]) * ax->fac[n0 + j], b = __uint_as_float(o[j + 1]) * ax->fac[n0 + j + 1];
-            const bool odd = (lane & 1u) != 0;
-            const float got = __shfl_xor_sync(0xffffffffu, odd ? a : b, 1);
-            const uint32_t w = odd ? pack_bf16(got, b) : pack_bf16(a, got);
-            const int n = n0 + j + (odd ? 1 : 0);
-            if (n < it.rows)
-              *reinterpret_cast<uint32_t*>(p.out + static_cast<int64_t>(it.row0 + n) * 512 + (d & ~1)) = w;
+              for (int j = 0; j < 16; ++j)
+                if (n0 + j < it.rows)
+                  dst32[static_cast<int64_t>(n0 + j) * 512 + d] = __uint_as_float(o[q][j]) * ax->fac[n0 + j];
+            }
+          } else {
+            // lane pairs exchange so that each stores two neighbouring dims of one row
+#pragma unroll
+            for (int j = 0; j < 16; j += 2) {
+              const float a = __uint_as_float(o[q][j]) * ax->fac[n0 + j];
+              const float b = __uint_as_float(o[q][j + 1]) * ax->fac[n0 + j + 1];
+              const bool odd = (lane & 1u) != 0;
+              const float got = __shfl_xor_sync(0xffffffffu, odd ? a : b, 1);
+              const uint32_t w = odd ? pack_bf16(got, b) : pack_bf16(a, got);
+              const int n = n0 + j + (odd ? 1 : 0);
+              if (n < it.rows)
+                *reinterpret_cast<uint32_t*>(p.out + static_cast<int64_t>(it.row0 + n) * 512 + (d & ~1)) = w;
+            }
           }
         }
       }
@@ -539,7 +548,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&ax->o_empty);
       }
-      soft_sync();          // fac and lim may be rewritten
+      bar_sync(1, kSoftThreads);          // fac and lim may be rewritten
     }
   }
   tc_fence_before();
@@ -587,52 +596,91 @@ __device__ __forceinline__ RowPieces row_pieces(const DenseMlaParams& p, int rec
   return x;
 }
 
-// A block of 128 threads per row, four dims a thread.
-__global__ void __launch_bounds__(128) dense_merge_kernel(const DenseMlaParams p, int N, int n_slots) {
+// WARPS warps per row, 4 x 4 dims a lane: one where there are many rows (their
+// loads overlap), the whole block where there are few, whose pieces it splits.
+template <int WARPS>
+__global__ void __launch_bounds__(256) dense_merge_kernel(const DenseMlaParams p, int N, int n_slots) {
+  __shared__ float4 part[WARPS > 1 ? WARPS : 1][128];
+  __shared__ float part_sum[WARPS];
   const float NEG_INF = __int_as_float(0xff800000);
   const int64_t rows = static_cast<int64_t>(min(max(__ldg(&p.cu_q[p.num_seqs]), 0), p.total_q)) * p.n_heads;
-  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
+  const int lane = static_cast<int>(threadIdx.x & 31u), warp = static_cast<int>(threadIdx.x >> 5);
+  constexpr int ROWS = 8 / WARPS;
+  const int w0 = warp % WARPS;
+  for (int64_t row = static_cast<int64_t>(blockIdx.x) * ROWS + warp / WARPS; row < rows;
+       row += static_cast<int64_t>(gridDim.x) * ROWS) {
     RowPieces a = row_pieces(p, 0, row, N, n_slots), b;
     b.n = 0;
     bool dead = false;
     if (p.shared) {
       b = row_pieces(p, 1, row, N, n_slots);
       dead = b.n == 0;                     // the row's sequence is out of range
-      if (p.prefix_len == 0) a.n = 0;
+      if (p.prefix_len == 0 || dead) a.n = 0;
     } else if (a.n == 0) {
       continue;                            // the main kernel wrote the row
     }
+    // the pieces' largest log-sum-exp, a piece per lane
     float m = NEG_INF;
-    for (int i = 0; i < a.n; ++i) m = fmaxf(m, a.lse[i == 0 ? 0 : a.lse_first + (i - 1) * a.lse_step]);
-    for (int i = 0; i < b.n; ++i) m = fmaxf(m, b.lse[i == 0 ? 0 : b.lse_first + (i - 1) * b.lse_step]);
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = lane; i < a.n; i += 32) m = fmaxf(m, a.lse[i == 0 ? 0 : a.lse_first + (i - 1) * a.lse_step]);
+    for (int i = lane; i < b.n; i += 32) m = fmaxf(m, b.lse[i == 0 ? 0 : b.lse_first + (i - 1) * b.lse_step]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float4 acc[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
     float sum = 0.f;
     const float ref = m == NEG_INF ? 0.f : m;
-    auto add = [&](const RowPieces& x) {
-#pragma unroll 4
-      for (int i = 0; i < x.n; ++i) {
-        const float z = x.lse[i == 0 ? 0 : x.lse_first + (i - 1) * x.lse_step];
-        if (z == NEG_INF) continue;
-        const float w = exp2f(z - ref);
-        const float4 o =
-            *reinterpret_cast<const float4*>(x.o + (i == 0 ? 0 : x.o_first + (i - 1) * x.o_step) + threadIdx.x * 4);
-        sum += w;
-        acc.x += w * o.x;
-        acc.y += w * o.y;
-        acc.z += w * o.z;
-        acc.w += w * o.w;
+    // piece j of a's and then b's
+#pragma unroll 2
+    for (int j = w0; j < a.n + b.n; j += WARPS) {
+      const RowPieces& x = j < a.n ? a : b;
+      const int i = j < a.n ? j : j - a.n;
+      const float z = x.lse[i == 0 ? 0 : x.lse_first + (i - 1) * x.lse_step];
+      if (z == NEG_INF) continue;          // an empty piece: its output was not written
+      const float w = exp2f(z - ref);
+      const float4* o = reinterpret_cast<const float4*>(x.o + (i == 0 ? 0 : x.o_first + (i - 1) * x.o_step)) + lane;
+      sum += w;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const float4 v = o[32 * c];
+        acc[c].x += w * v.x;
+        acc[c].y += w * v.y;
+        acc[c].z += w * v.z;
+        acc[c].w += w * v.w;
       }
-    };
-    if (!dead) {
-      add(a);
-      add(b);
+    }
+    if constexpr (WARPS > 1) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) part[w0][32 * c + lane] = acc[c];
+      if (lane == 0) part_sum[w0] = sum;
+      __syncthreads();
+      sum = 0.f;
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) sum += part_sum[w];
+      // four warps store 128 dims each
+      if (w0 < 4) {
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) {
+          const float4 u = part[w][32 * w0 + lane];
+          v.x += u.x;
+          v.y += u.y;
+          v.z += u.z;
+          v.w += u.w;
+        }
+        acc[0] = v;
+      }
+      __syncthreads();
     }
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    uint2 w;
-    w.x = pack_bf16(acc.x * inv, acc.y * inv);
-    w.y = pack_bf16(acc.z * inv, acc.w * inv);
-    *reinterpret_cast<uint2*>(p.out + row * 512 + threadIdx.x * 4) = w;
-    if (threadIdx.x == 0 && p.lse != nullptr) p.lse[row] = sum == 0.f ? NEG_INF : (ref + log2f(sum)) * kLn2;
+#pragma unroll
+    for (int c = 0; c < (WARPS > 1 ? 1 : 4); ++c) {
+      uint2 w;
+      w.x = pack_bf16(acc[c].x * inv, acc[c].y * inv);
+      w.y = pack_bf16(acc[c].z * inv, acc[c].w * inv);
+      if (w0 < 4) *reinterpret_cast<uint2*>(p.out + row * 512 + (WARPS > 1 ? w0 : c) * 128 + lane * 4) = w;
+    }
+    if (w0 == 0 && lane == 0 && p.lse != nullptr) p.lse[row] = sum == 0.f ? NEG_INF : (ref + log2f(sum)) * kLn2;
   }
 }
 
@@ -675,8 +723,14 @@ cudaError_t launch_dense_mla(const DenseMlaParams& p, const DensePlan& d, const 
   }
   if (e != cudaSuccess) return e;
   const int64_t rows = static_cast<int64_t>(p.total_q) * p.n_heads;
-  const int grid = static_cast<int>(rows < 148 * 16 ? rows : 148 * 16);
-  dense_merge_kernel<<<grid, 128, 0, stream>>>(p, d.n, dense_slots(d.n));
+  const bool few = rows <= 4 * 148;
+  const int64_t blocks = few ? rows : (rows + 7) / 8;
+  const int grid = static_cast<int>(blocks < 148 * 8 ? blocks : 148 * 8);
+  if (few) {
+    dense_merge_kernel<8><<<grid, 256, 0, stream>>>(p, d.n, dense_slots(d.n));
+  } else {
+    dense_merge_kernel<1><<<grid, 256, 0, stream>>>(p, d.n, dense_slots(d.n));
+  }
   return cudaGetLastError();
 }
 

@@ -218,6 +218,7 @@ struct DenseMlaParams {
   int32_t gang = 1;                   // CTAs that walk the same keys with neighbouring row tiles
   int32_t shared = 0;                 // the first prefix_len positions are sequence 0's for every sequence
   int32_t prefix_len = 0;
+  const uint16_t* kv = nullptr;       // bf16 [total_keys, 576]
   float scale_log2 = 0.f;             // sm_scale * log2(e)
   uint16_t* out = nullptr;            // bf16 [total_q, H, 512]
   float* lse = nullptr;               // [total_q, H] or nullptr
