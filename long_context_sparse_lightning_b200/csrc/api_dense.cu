@@ -77,12 +77,14 @@ dsa_status_t run_dense(const dsa_batch_t* b, int prefix_len, const void* q, int 
   p.row_o = reinterpret_cast<float*>(base + l.row_o);
   p.err = reinterpret_cast<uint32_t*>(base);
   p.budget = dsa::wait_budget();
-  CUtensorMap map_q, map_c;
-  if (!dsa::make_tmap_bf16(&map_q, q, static_cast<uint64_t>(b->total_q) * n_heads, 576, 576,
-                           dsa::dense_q_box(d.n)) ||
-      !dsa::make_tmap_bf16(&map_c, kv, static_cast<uint64_t>(b->total_keys), 576, 576, dsa::dense_c_box(d.n)))
+  const bool pair = d.n == 128;
+  const uint64_t rows = static_cast<uint64_t>(b->total_q) * n_heads, keys = static_cast<uint64_t>(b->total_keys);
+  dsa::DenseMaps maps;
+  if (!dsa::make_tmap_blocks(&maps.q, q, rows, 9, 576, pair ? 64 : d.n, 9) ||
+      !dsa::make_tmap_blocks(&maps.c, kv, keys, 9, 576, pair ? 32 : 64, pair ? 9 : 2) ||
+      !dsa::make_tmap_blocks(&maps.v, kv, keys, 9, 576, pair ? 32 : 64, pair ? 4 : 1))
     return DSA_ERR_CUDA;
-  return dsa::launch_dense_mla(p, d, map_q, map_c, stream) == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+  return dsa::launch_dense_mla(p, d, maps, stream) == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 }
 
 }  // namespace
@@ -139,10 +141,10 @@ dsa_status_t dsa_expanded_mla(const dsa_batch_t* b, const void* q, int32_t n_hea
   p.budget = dsa::wait_budget();
   const uint64_t h = static_cast<uint64_t>(n_heads);
   CUtensorMap map_q, map_kv, map_r;
-  if (!dsa::make_tmap_bf16(&map_q, q, static_cast<uint64_t>(b->total_q), h * 192, h * 192, 128) ||
-      !dsa::make_tmap_bf16(&map_kv, kv_up, static_cast<uint64_t>(b->total_keys), h * 256, h * 256, 128) ||
-      !dsa::make_tmap_bf16(&map_r, rope, static_cast<uint64_t>(b->total_keys), 64, static_cast<uint64_t>(rope_stride),
-                           128))
+  if (!dsa::make_tmap_blocks(&map_q, q, static_cast<uint64_t>(b->total_q), h * 3, h * 192, 128, 3) ||
+      !dsa::make_tmap_blocks(&map_kv, kv_up, static_cast<uint64_t>(b->total_keys), h * 4, h * 256, 128, 1) ||
+      !dsa::make_tmap_blocks(&map_r, rope, static_cast<uint64_t>(b->total_keys), 1, static_cast<uint64_t>(rope_stride),
+                             128, 1))
     return DSA_ERR_CUDA;
   return dsa::launch_expanded_mla(p, b->max_q_per_seq, map_q, map_kv, map_r, reinterpret_cast<cudaStream_t>(stream)) ==
                  cudaSuccess

@@ -137,7 +137,7 @@ __device__ __forceinline__ Entry make_entry(const DenseMlaParams& p, int v, cons
         e.status = 503;                             // the sequence does not hold the whole prefix
     }
   }
-  e.gangs = (e.rows + N * p.gang - 1) / (N * p.gang);
+  e.gangs = e.rows <= N * p.gang ? (e.rows > 0 ? 1 : 0) : (e.rows + N * p.gang - 1) / (N * p.gang);
   return e;
 }
 
@@ -148,7 +148,7 @@ __device__ __forceinline__ Entry entry_at(const DenseMlaParams& p, int v) {
 
 // Last position the rows [.., row_end) of the entry see.
 __device__ __forceinline__ int last_seen(const DenseMlaParams& p, const Entry& e, int row_end) {
-  if (e.prefix) return e.kv - 1;
+  if (e.prefix || row_end == e.rows) return e.kv - 1;      // (divisions are left out where they can be)
   return e.kv - e.q_len + (row_end - 1) / p.n_heads;
 }
 
@@ -206,74 +206,83 @@ __device__ __forceinline__ Share find_share(const DenseMlaParams& p, ShareScratc
                                             int n_units) {
   constexpr int WARPS = THREADS / 32;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int n_entries = p.num_seqs + (p.shared ? 1 : 0);
-  long long mine = 0, cost0 = 0;
-  Entry e0{};
-  for (int v = tid; v < n_entries; v += THREADS) {
-    const Entry e = v == tid ? make_entry<N>(p, v, first) : entry_at<N>(p, v);
-    const long long c = entry_cost<N>(p, e);
-    if (blockIdx.x == 0 && e.status != 0) report_error(p.err, kDevErrBounds, e.status, e.b);
-    mine += c;
-    if (v == tid) {
-      e0 = e;
-      cost0 = c;
+  const int n_entries = p.num_seqs + p.shared;
+  // the block's running sum of `c`: this thread's start, and the sum over all
+  auto scan = [&](long long c, long long& all) -> long long {
+    long long inc = c;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long t = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += t;
     }
+    if (lane == 31) sc.scan[warp] = inc;
+    __syncthreads();
+    long long before = 0;
+    all = 0;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+      const long long t = sc.scan[w];
+      if (w < warp) before += t;
+      all += t;
+    }
+    return before + inc - c;
+  };
+  auto cost_of = [&](const Entry& e) {
+    if (blockIdx.x == 0 && e.status != 0) report_error(p.err, kDevErrBounds, e.status, e.b);
+    return entry_cost<N>(p, e);
+  };
+  Entry e{};
+  long long c = 0, total = 0;
+  if (tid < n_entries) {
+    e = make_entry<N>(p, tid, first);
+    c = cost_of(e);
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-  if (lane == 0) sc.scan[warp] = mine;
   if (tid == 0) sc.entry = -1;
-  __syncthreads();
+  long long start = scan(c, total);
+  // more entries than threads: the others' sum (each is read again below)
+  if (n_entries > THREADS) {
+    long long more = 0, sum;
+    for (int v = tid + THREADS; v < n_entries; v += THREADS) more += cost_of(entry_at<N>(p, v));
+    __syncthreads();
+    scan(more, sum);
+    total += sum;
+  }
   Share s;
-  long long total = 0;
-#pragma unroll
-  for (int w = 0; w < WARPS; ++w) total += sc.scan[w];
-  s.gang = unit / p.gang;
+  s.gang = p.gang == 1 ? unit : unit / p.gang;
   s.member = unit - s.gang * p.gang;
-  s.gangs = static_cast<int>(
-      min(static_cast<long long>(n_units / p.gang), max(1LL, (total + kMinShare - 1) / kMinShare)));
+  s.gangs = static_cast<int>(min(static_cast<long long>(p.gang == 1 ? n_units : n_units / p.gang),
+                                 max(1LL, (total + kMinShare - 1) / kMinShare)));
   s.per = divide(total, s.gangs);
   s.rem = static_cast<int>(total - s.per * s.gangs);
   s.lo = s.gang < s.gangs ? s.gang * s.per + min(s.gang, s.rem) : total;
   s.hi = s.gang < s.gangs ? s.lo + s.per + (s.gang < s.rem ? 1 : 0) : total;
-  __syncthreads();
   if (s.lo < s.hi) {
-    long long base = 0;
-    for (int v0 = 0; v0 < n_entries; v0 += THREADS) {
-      const int v = v0 + tid;
-      long long c = cost0;
-      if (v0 > 0) {
-        c = 0;
-        if (v < n_entries) {
-          e0 = entry_at<N>(p, v);
-          c = entry_cost<N>(p, e0);
-        }
-      }
-      long long inc = c;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long t = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += t;
-      }
-      if (lane == 31) sc.scan[warp] = inc;
-      __syncthreads();
-      long long before = base, all = 0;
-#pragma unroll
-      for (int w = 0; w < WARPS; ++w) {
-        if (w < warp) before += sc.scan[w];
-        all += sc.scan[w];
-      }
-      const long long start = before + inc - c;
+    // the entry that holds lo
+    long long base = 0, all = 0;
+    for (int v0 = 0;;) {
       if (c > 0 && start <= s.lo && s.lo < start + c) {
-        sc.entry = v;
+        sc.entry = v0 + tid;
         sc.start = start;
-        sc.e = e0;
+        sc.e = e;
+      }
+      v0 += THREADS;
+      if (v0 >= n_entries) break;
+      if (v0 == THREADS) {           // the first chunk's sum, from its scan
+        __syncthreads();
+        scan(c, all);
       }
       base += all;
+      if (base > s.lo) break;        // uniform
       __syncthreads();
-      if (base > s.lo) break;      // uniform
+      c = 0;
+      if (v0 + tid < n_entries) {
+        e = entry_at<N>(p, v0 + tid);
+        c = entry_cost<N>(p, e);
+      }
+      start = base + scan(c, all);
     }
   }
+  __syncthreads();
   s.entry = s.lo < s.hi ? sc.entry : -1;
   s.start = s.entry >= 0 ? sc.start : 0;
   s.e = sc.e;

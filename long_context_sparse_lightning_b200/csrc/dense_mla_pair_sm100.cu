@@ -92,8 +92,7 @@ __device__ __forceinline__ void store_32(void* dst, const uint32_t (&v)[8]) {
 }
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    dense_pair_kernel(const DenseMlaParams p, const __grid_constant__ CUtensorMap map_q,
-                      const __grid_constant__ CUtensorMap map_c) {
+    dense_pair_kernel(const DenseMlaParams p, const __grid_constant__ DenseMaps maps) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   uint8_t* sm = smem_raw + (((raw + 1023u) & ~1023u) - raw);
@@ -127,15 +126,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     mbar_init(&ax->o_full, 1);
     mbar_init(&ax->o_free, 16);
     fence_mbar_init();
-    prefetch_tmap(&map_q);
-    prefetch_tmap(&map_c);
+    prefetch_tmap(&maps.q);
+    prefetch_tmap(&maps.c);
+    prefetch_tmap(&maps.v);
   }
   if (warp == 1) tmem_alloc_pair(&ax->tmem, kTmemCols);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const Share share = find_share<kN, kThreads>(p, ax->share, first, unit, n_units);
-  __syncthreads();
   cluster_sync();                                      // the other CTA's barriers exist
   const uint32_t tmem = ax->tmem;
 
@@ -163,17 +162,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     Walk<kN> walk(p, share, unit);
     Item it;
     while (ok && walk.next(it)) {
-      publish(it);
-      if (!ok || it.n_tiles == 0) continue;
-      if (n_q > 0) wait(&ax->q_free, (n_q - 1) & 1, 551);
-      if (!ok) break;
-      ++n_q;
-      if (lane == 0) {
-        if (rank == 0) mbar_arrive_expect_tx(&ax->q_full, 2 * 9 * kQBlk);
-        for (int c = 0; c < 9; ++c)
-          tma_load_2d_pair(sm + OFF_Q + c * kQBlk, &map_q, q_full, c * 64, it.row0 + 64 * static_cast<int>(rank));
-      }
-      __syncwarp();
       const int64_t kstart = walk.e.kstart;
       // Cache rows of 32 tiles, one per lane (a tile lies in one page), and of the 32 after them.
       auto tile_row = [&](int i) -> int {
@@ -183,6 +171,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         return r < 0 ? -1 : static_cast<int>(r);
       };
       int my_row = tile_row(static_cast<int>(lane)), my_next = tile_row(32 + static_cast<int>(lane));
+      publish(it);
+      if (!ok || it.n_tiles == 0) continue;
+      if (n_q > 0) wait(&ax->q_free, (n_q - 1) & 1, 551);
+      if (!ok) break;
+      ++n_q;
+      if (lane == 0) {
+        if (rank == 0) mbar_arrive_expect_tx(&ax->q_full, 2 * 9 * kQBlk);
+        tma_load_3d_pair(sm + OFF_Q, &maps.q, q_full, 0, it.row0 + 64 * static_cast<int>(rank), 0);
+      }
+      __syncwarp();
       for (int i = 0; ok && i < it.n_tiles; ++i, ++t) {
         if (i > 0 && (i & 31) == 0) {
           my_row = my_next;
@@ -201,7 +199,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const uint32_t full = mapa_shared(smem_u32(&ax->full[s]), 0);
           // a tile of a page outside the pool lies behind the cache: zeros arrive, no row is read
           const int y = row < 0 ? static_cast<int>(p.total_keys) : row + 32 * static_cast<int>(rank);
-          for (int d = 0; d < 9; ++d) tma_load_2d_pair(sm + OFF_KV + s * kStage + d * kBlk, &map_c, full, d * 64, y);
+          tma_load_3d_pair(sm + OFF_KV + s * kStage, &maps.c, full, 0, y, 0);
         }
         // this CTA's keys of a later tile: 288 lines of one run of the cache, nine per lane
         const int ahead = (i & 31) + kPrefetch < 32 ? ahead_a : ahead_b;
@@ -327,9 +325,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           mbar_arrive_expect_tx(&ax->v_full[s], (border ? 8 : 4) * kBlk);
           for (int g = 0; g < 2; ++g) {
             if (!border && g == static_cast<int>(rank)) continue;
-            for (int c = 0; c < 4; ++c)
-              tma_load_2d(st + (4 * g + c) * kBlk, &map_c, &ax->v_full[s], 256 * static_cast<int>(rank) + 64 * c,
-                          row < 0 ? none : row + 32 * g);
+            tma_load_3d(st + 4 * g * kBlk, &maps.v, &ax->v_full[s], 0, row < 0 ? none : row + 32 * g,
+                        4 * static_cast<int>(rank));
           }
         }
         __syncwarp();
@@ -581,8 +578,7 @@ int resident_pairs() {
 
 }  // namespace
 
-cudaError_t launch_dense_pair(const DenseMlaParams& p, const CUtensorMap& map_q, const CUtensorMap& map_c,
-                              cudaStream_t stream) {
+cudaError_t launch_dense_pair(const DenseMlaParams& p, const DenseMaps& maps, cudaStream_t stream) {
   cudaError_t e = cudaFuncSetAttribute(dense_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
   int pairs = resident_pairs();
@@ -590,7 +586,7 @@ cudaError_t launch_dense_pair(const DenseMlaParams& p, const CUtensorMap& map_q,
   if (pairs < 1 || pairs > kDenseMaxCtas / 2) pairs = kDenseMaxCtas / 2;
   if (pairs < p.gang) return cudaErrorInvalidConfiguration;
   pairs = pairs / p.gang * p.gang;
-  dense_pair_kernel<<<2 * pairs, kThreads, kSmem, stream>>>(p, map_q, map_c);
+  dense_pair_kernel<<<2 * pairs, kThreads, kSmem, stream>>>(p, maps);
   return cudaGetLastError();
 }
 

@@ -119,8 +119,7 @@ __device__ __forceinline__ void ld_cols16(uint32_t t, uint32_t (&r)[16]) {
 
 template <int N>
 __global__ void __launch_bounds__(kThreads, 1)
-    dense_mla_kernel(const DenseMlaParams p, const __grid_constant__ CUtensorMap map_q,
-                     const __grid_constant__ CUtensorMap map_c) {
+    dense_mla_kernel(const DenseMlaParams p, const __grid_constant__ DenseMaps maps) {
   using C = Cfg<N>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -153,8 +152,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&ax->o_full, 1);
     mbar_init(&ax->o_empty, 4);
     fence_mbar_init();
-    prefetch_tmap(&map_q);
-    prefetch_tmap(&map_c);
+    prefetch_tmap(&maps.q);
+    prefetch_tmap(&maps.c);
+    prefetch_tmap(&maps.v);
   }
   if (warp == 1) {
     tmem_alloc(&ax->tmem, kTmemCols);
@@ -165,7 +165,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const Share share = find_share<N, kThreads>(p, ax->share, first, static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x));
-  __syncthreads();
   const uint32_t tmem = ax->tmem;
 
   if (warp == 0) {
@@ -191,6 +190,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     Walk<N> walk(p, share, static_cast<int>(blockIdx.x));
     Item it;
     while (ok && walk.next(it)) {
+      // Cache rows of 32 tiles, one per lane (a tile lies in one page), and of the 32 after them.
+      auto tile_row = [&](int i) -> int {
+        if (i >= it.n_tiles) return -1;
+        const int64_t r = cache_row(p.pt, walk.e.b, walk.e.kstart, (it.tile0 + i) * kKeys);
+        if (r < 0) report_error(p.err, kDevErrBounds, 504, walk.e.b);
+        return r < 0 ? -1 : static_cast<int>(r);
+      };
+      int my_row = tile_row(static_cast<int>(lane)), my_next = tile_row(32 + static_cast<int>(lane));
       publish(it);
       if (!ok || it.n_tiles == 0) continue;
       if (n_q > 0) wait(&ax->q_free, (n_q - 1) & 1, 511);
@@ -198,17 +205,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++n_q;
       if (lane == 0) {
         mbar_arrive_expect_tx(&ax->q_full, 9 * N * 128);
-        for (int c = 0; c < 9; ++c) tma_load_2d(sm + C::OFF_Q + c * N * 128, &map_q, &ax->q_full, c * 64, it.row0);
+        tma_load_3d(sm + C::OFF_Q, &maps.q, &ax->q_full, 0, it.row0, 0);
       }
       __syncwarp();
-      const int64_t kstart = walk.e.kstart;
-      int my_row = 0;
       for (int i = 0; ok && i < it.n_tiles; ++i) {
-        if ((i & 31) == 0) {            // cache rows of the next 32 tiles, one per lane (a tile lies in one page)
-          const int t = min(i + static_cast<int>(lane), it.n_tiles - 1);
-          const int64_t r = cache_row(p.pt, walk.e.b, kstart, (it.tile0 + t) * kKeys);
-          if (r < 0) report_error(p.err, kDevErrBounds, 504, walk.e.b);
-          my_row = r < 0 ? -1 : static_cast<int>(r);
+        if (i > 0 && (i & 31) == 0) {
+          my_row = my_next;
+          my_next = tile_row(i + 32 + static_cast<int>(lane));
         }
         int row = __shfl_sync(0xffffffffu, my_row, i & 31);
         const int skip = row < 0 ? 1 : 0;
@@ -218,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         if (lane == 0) {
           mbar_arrive_expect_tx(&ax->rope_full[rs], kBlk);
-          tma_load_2d(sm + C::OFF_ROPE + rs * kBlk, &map_c, &ax->rope_full[rs], 512, row);
+          tma_load_3d(sm + C::OFF_ROPE + rs * kBlk, &maps.v, &ax->rope_full[rs], 0, row, 8);
         }
         ++n_rope;
         for (int m = 0; ok && m < 4; ++m) {
@@ -229,8 +232,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint8_t* dst = sm + C::OFF_PAIR + ps * kPair;
             if (m == 0) ax->skip[ps] = skip;
             mbar_arrive_expect_tx(&ax->pair_full[ps], kPair);
-            tma_load_2d(dst, &map_c, &ax->pair_full[ps], m * 128, row);
-            tma_load_2d(dst + kBlk, &map_c, &ax->pair_full[ps], m * 128 + 64, row);
+            tma_load_3d(dst, &maps.c, &ax->pair_full[ps], 0, row, 2 * m);
           }
           ++n_pair;
         }
@@ -685,11 +687,10 @@ __global__ void __launch_bounds__(256) dense_merge_kernel(const DenseMlaParams p
 }
 
 template <int N>
-cudaError_t launch(const DenseMlaParams& p, const CUtensorMap& map_q, const CUtensorMap& map_c, int ctas,
-                   cudaStream_t stream) {
+cudaError_t launch(const DenseMlaParams& p, const DenseMaps& maps, int ctas, cudaStream_t stream) {
   cudaError_t e = cudaFuncSetAttribute(dense_mla_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<N>::SMEM);
   if (e != cudaSuccess) return e;
-  dense_mla_kernel<N><<<ctas, kThreads, Cfg<N>::SMEM, stream>>>(p, map_q, map_c);
+  dense_mla_kernel<N><<<ctas, kThreads, Cfg<N>::SMEM, stream>>>(p, maps);
   return cudaGetLastError();
 }
 
@@ -710,16 +711,15 @@ DensePlan dense_plan(const dsa_batch_t* b, int n_heads, bool shared) {
   return d;
 }
 
-cudaError_t launch_dense_mla(const DenseMlaParams& p, const DensePlan& d, const CUtensorMap& map_q,
-                             const CUtensorMap& map_c, cudaStream_t stream) {
+cudaError_t launch_dense_mla(const DenseMlaParams& p, const DensePlan& d, const DenseMaps& maps, cudaStream_t stream) {
   cudaError_t e;
   if (d.n == 128) {
-    e = launch_dense_pair(p, map_q, map_c, stream);
+    e = launch_dense_pair(p, maps, stream);
   } else {
     int ctas = sm_count();
     if (ctas < 1 || ctas > kDenseMaxCtas) ctas = kDenseMaxCtas;
     ctas = ctas / p.gang * p.gang;
-    e = d.n == 16 ? launch<16>(p, map_q, map_c, ctas, stream) : launch<32>(p, map_q, map_c, ctas, stream);
+    e = d.n == 16 ? launch<16>(p, maps, ctas, stream) : launch<32>(p, maps, ctas, stream);
   }
   if (e != cudaSuccess) return e;
   const int64_t rows = static_cast<int64_t>(p.total_q) * p.n_heads;

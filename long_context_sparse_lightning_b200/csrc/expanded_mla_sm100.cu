@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (elect_one()) {
         bool ok = true;
         int n = 0;
-        auto load = [&](const CUtensorMap* m, int x, int y) {
+        auto load = [&](const CUtensorMap* m, int block, int y) {
           const int s = n % kSlots;
           if (ok && n >= kSlots && !mbar_wait(&ax->empty[s], ((n / kSlots) + 1) & 1, p.budget)) {
             report_error(p.err, kDevErrTimeout, 611, blockIdx.x);
@@ -163,28 +163,27 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (!ok) return;
           mbar_arrive_expect_tx(&ax->full[s], kBlk);
-          tma_load_2d(sm + OFF_KV + s * kBlk, m, &ax->full[s], x, y);
+          tma_load_3d(sm + OFF_KV + s * kBlk, m, &ax->full[s], 0, y, block);
           ++n;
         };
         for (int a = 0; a < (two ? 2 : 1); ++a) {
           mbar_arrive_expect_tx(&ax->q_full[a], 3 * kBlk);
-          for (int c = 0; c < 3; ++c)
-            tma_load_2d(sm + OFF_Q + (3 * a + c) * kBlk, &map_q, &ax->q_full[a], h * 192 + c * 64, w.row0 + a * kRows);
+          tma_load_3d(sm + OFF_Q + 3 * a * kBlk, &map_q, &ax->q_full[a], 0, w.row0 + a * kRows, h * 3);
           if (a == 0) {
-            load(&map_kv, h * 256, w.first_row_key);
-            load(&map_kv, h * 256 + 64, w.first_row_key);
+            load(&map_kv, h * 4, w.first_row_key);
+            load(&map_kv, h * 4 + 1, w.first_row_key);
             load(&map_r, 0, w.first_row_key);
           }
         }
         for (int i = 0; ok && i < n_tiles; ++i) {
           const int y = w.first_row_key + i * kKeys;
           if (i > 0) {
-            load(&map_kv, h * 256, y);
-            load(&map_kv, h * 256 + 64, y);
+            load(&map_kv, h * 4, y);
+            load(&map_kv, h * 4 + 1, y);
             load(&map_r, 0, y);
           }
-          load(&map_kv, h * 256 + 128, y);
-          load(&map_kv, h * 256 + 192, y);
+          load(&map_kv, h * 4 + 2, y);
+          load(&map_kv, h * 4 + 3, y);
         }
         if (!ok) {      // let the copies in flight land before the block ends
           bool landed = true;

@@ -27,9 +27,12 @@ struct PageTable {
 // argument checks (DSA_OK or the status to return) and its page table.
 dsa_status_t validate_batch(const dsa_batch_t* b);
 PageTable batch_pages(const dsa_batch_t* b);
-// TMA descriptor of a row-major [rows, cols] view of 16-bit elements whose rows are
-// `ld` elements apart, box [box_rows, 64], 128-byte swizzle; false if refused.
-bool make_tmap_bf16(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint64_t ld, uint32_t box_rows);
+// TMA descriptor of a row-major [rows, 64 * blocks] matrix of 16-bit elements whose
+// rows are `ld` elements apart, seen as (64 elements, rows, blocks): a box of
+// box_blocks x box_rows x 64 lands as that many [box_rows x 64] blocks one after
+// the other, 128-byte swizzle each; false if refused.
+bool make_tmap_blocks(CUtensorMap* m, const void* base, uint64_t rows, uint64_t blocks, uint64_t ld, uint32_t box_rows,
+                      uint32_t box_blocks);
 #ifdef __CUDACC__
 // First cache row of sequence b (flat caches; 0 when paged, where kv_start
 // may be null).
@@ -239,17 +242,17 @@ struct DensePlan {
   int gang;
 };
 DensePlan dense_plan(const dsa_batch_t* b, int n_heads, bool shared);
-// The attention and the merge of its split items.  map_q: q as [total_q * H, 576],
-// box [dense_q_box(N) rows x 64]; map_c: the cache [total_keys, 576], box
-// [dense_c_box(N) rows x 64]; both 128-byte swizzle.
-inline uint32_t dense_q_box(int n) { return n == 128 ? 64u : static_cast<uint32_t>(n); }
-inline uint32_t dense_c_box(int n) { return n == 128 ? 32u : 64u; }
-cudaError_t launch_dense_mla(const DenseMlaParams& p, const DensePlan& d, const CUtensorMap& map_q,
-                             const CUtensorMap& map_c, cudaStream_t stream);
-
+// TMA descriptors (see make_tmap_blocks) of q as [total_q * H, 576] and of the cache
+// [total_keys, 576]: boxes of blocks x rows
+//   N = 16, 32:  q 9 x N,   c 2 x 64 (128 value dims of a tile), v 1 x 64 (its RoPE dims)
+//   N = 128:     q 9 x 64,  c 9 x 32 (a CTA's keys of a tile), v 4 x 32 (its dims of the other's)
+struct DenseMaps {
+  CUtensorMap q, c, v;
+};
+// The attention and the merge of its split items.
+cudaError_t launch_dense_mla(const DenseMlaParams& p, const DensePlan& d, const DenseMaps& maps, cudaStream_t stream);
 // its CTA-pair kernel (N = 128)
-cudaError_t launch_dense_pair(const DenseMlaParams& p, const CUtensorMap& map_q, const CUtensorMap& map_c,
-                              cudaStream_t stream);
+cudaError_t launch_dense_pair(const DenseMlaParams& p, const DenseMaps& maps, cudaStream_t stream);
 
 // ----------------------------------------------------------- expanded MLA --
 struct ExpandedMlaParams {
@@ -267,8 +270,8 @@ struct ExpandedMlaParams {
   uint32_t* err = nullptr;
   long long budget = 2000000000LL;
 };
-// map_q: q as [total_q, H * 192]; map_kv: [total_keys, H * 256]; map_r: the RoPE
-// dims [total_keys, 64]; boxes of [128 rows x 64], 128-byte swizzle.
+// Descriptors (see make_tmap_blocks) of q as [total_q, H * 192], boxes of 3 x 128;
+// kv_up as [total_keys, H * 256] and the RoPE dims [total_keys, 64], boxes of 1 x 128.
 cudaError_t launch_expanded_mla(const ExpandedMlaParams& p, int max_q_per_seq, const CUtensorMap& map_q,
                                 const CUtensorMap& map_kv, const CUtensorMap& map_r, cudaStream_t stream);
 
