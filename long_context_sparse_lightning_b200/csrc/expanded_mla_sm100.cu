@@ -16,18 +16,15 @@
 // (2560 cycles at full rate) and the 2 x 128 x 128 exponentials take 2048 at
 // 16 per cycle, so both units have to be kept busy at once.
 //
-// Roles: warp 0 TMA, warp 1 MMAs, warps 2-3 clean the value tiles on the border
-// (below), warps 4-7 and 8-11 softmax and epilogue of the two tiles.
+// Roles: warp 0 TMA, warp 1 MMAs of both tiles, warps 2-3 clean the value
+// tiles on the border (below), warps 4-7 and 8-11 softmax and epilogue of the tiles.
 //
 // A position that some row of the CTA must not see has probability 0 there,
 // and 0 x a non-finite value would reach that row all the same.  So in tiles on
 // the border the cleaning warps zero the value rows that no row of the CTA
 // sees, and for a non-finite value at a position that only later rows see they
 // zero it and note the first such position per dim: rows that do see it get NaN.
-#include <cuda_bf16.h>
-
-#include "kernels.cuh"
-#include "ptx.cuh"
+#include "dense_mla.cuh"
 
 namespace dsa {
 namespace {
@@ -35,11 +32,10 @@ namespace {
 constexpr int kRows = 128;                 // query rows per tile (TMEM lanes)
 constexpr int kKeys = 128;                 // keys per tile
 constexpr int kBlk = 128 * 128;            // one [128 rows x 64 dims] block, 128-byte swizzle
-constexpr int kSlots = 8;                  // key / value blocks in flight: 3 + 2 per tile
+constexpr int kSlots = 8;                  // ring of key / value blocks, 3 + 2 per tile
+__device__ __forceinline__ int ring(int block) { return block & (kSlots - 1); }
 constexpr int kThreads = 12 * 32;
 constexpr uint32_t kRegLow = 88, kRegHigh = 208;     // 128 * (88 + 2 * 208) = 384 * 168
-constexpr float kGrow = 24.f;              // log2 units a score may exceed its row's reference by
-constexpr float kLn2 = 0.69314718055994531f;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t TM_S = 0, TM_O = 256;   // + 128 * tile
 
@@ -51,23 +47,19 @@ static_assert(kSmem <= 232448, "shared memory of one CTA");
 
 struct Aux {
   uint64_t q_full[2];
-  uint64_t full[kSlots], empty[kSlots];
+  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];      // by tile parity
   uint64_t s_full[2], p_full[2], o_done[2];
-  uint64_t go, clean;       // border tiles: the values have landed / are clean
+  uint64_t go, clean;       // the values before the border have landed / a border tile's are clean
   uint32_t tmem;
   int32_t bad_pos[128];     // first position whose value of this dim is not finite, per dim
 };
 static_assert(sizeof(Aux) <= 1024, "");
 
-__device__ __forceinline__ float exp2_approx(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
+using dense::exp2_approx;
+using dense::finite_or_zero;
+using dense::kGrow;
+using dense::kLn2;
+using dense::pack_bf16;
 
 // What a CTA works on.
 struct Tile {
@@ -127,9 +119,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&ax->p_full[i], 4);
       mbar_init(&ax->o_done[i], 1);
     }
-    for (int i = 0; i < kSlots; ++i) {
-      mbar_init(&ax->full[i], 1);
-      mbar_init(&ax->empty[i], 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ax->k_full[i], 1);
+      mbar_init(&ax->v_full[i], 1);
+      mbar_init(&ax->k_empty[i], 1);
+      mbar_init(&ax->v_empty[i], 1);
     }
     mbar_init(&ax->go, 1);
     mbar_init(&ax->clean, 2);
@@ -154,50 +148,68 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ----------------------------------------------------------------- TMA --
       if (elect_one()) {
         bool ok = true;
-        int n = 0;
-        auto load = [&](const CUtensorMap* m, int block, int y) {
-          const int s = n % kSlots;
-          if (ok && n >= kSlots && !mbar_wait(&ax->empty[s], ((n / kSlots) + 1) & 1, p.budget)) {
+        auto wait = [&](uint64_t* bar, uint32_t parity) {
+          if (ok && !mbar_wait(bar, parity, p.budget)) {
             report_error(p.err, kDevErrTimeout, 611, blockIdx.x);
             ok = false;
           }
-          if (!ok) return;
-          mbar_arrive_expect_tx(&ax->full[s], kBlk);
-          tma_load_3d(sm + OFF_KV + s * kBlk, m, &ax->full[s], 0, y, block);
-          ++n;
+          return ok;
+        };
+        int n_k = 0, n_v = 0;
+        auto keys = [&](int i) {
+          // blocks 5 i .. 5 i + 2 of the ring take the place of the last of K(i - 2) and of V(i - 2)
+          if (i >= 2 && !wait(&ax->v_empty[i & 1], ((i >> 1) + 1) & 1)) return;
+          uint64_t* bar = &ax->k_full[i & 1];
+          const int y = w.first_row_key + i * kKeys;
+          mbar_arrive_expect_tx(bar, 3 * kBlk);
+          tma_load_3d(sm + OFF_KV + ring(5 * i) * kBlk, &map_kv, bar, 0, y, h * 4);
+          tma_load_3d(sm + OFF_KV + ring(5 * i + 1) * kBlk, &map_kv, bar, 0, y, h * 4 + 1);
+          tma_load_3d(sm + OFF_KV + ring(5 * i + 2) * kBlk, &map_r, bar, 0, y, 0);
+          ++n_k;
+        };
+        auto values = [&](int i) {
+          // blocks 5 i + 3 and 5 i + 4 that of the first two of K(i - 1)
+          if (i >= 1 && !wait(&ax->k_empty[(i - 1) & 1], ((i - 1) >> 1) & 1)) return;
+          uint64_t* bar = &ax->v_full[i & 1];
+          const int y = w.first_row_key + i * kKeys;
+          mbar_arrive_expect_tx(bar, 2 * kBlk);
+          tma_load_3d(sm + OFF_KV + ring(5 * i + 3) * kBlk, &map_kv, bar, 0, y, h * 4 + 2);
+          tma_load_3d(sm + OFF_KV + ring(5 * i + 4) * kBlk, &map_kv, bar, 0, y, h * 4 + 3);
+          ++n_v;
         };
         for (int a = 0; a < (two ? 2 : 1); ++a) {
           mbar_arrive_expect_tx(&ax->q_full[a], 3 * kBlk);
           tma_load_3d(sm + OFF_Q + 3 * a * kBlk, &map_q, &ax->q_full[a], 0, w.row0 + a * kRows, h * 3);
-          if (a == 0) {
-            load(&map_kv, h * 4, w.first_row_key);
-            load(&map_kv, h * 4 + 1, w.first_row_key);
-            load(&map_r, 0, w.first_row_key);
-          }
+          if (a == 0) keys(0);
         }
-        for (int i = 0; ok && i < n_tiles; ++i) {
-          const int y = w.first_row_key + i * kKeys;
-          if (i > 0) {
-            load(&map_kv, h * 4, y);
-            load(&map_kv, h * 4 + 1, y);
-            load(&map_r, 0, y);
-          }
-          load(&map_kv, h * 4 + 2, y);
-          load(&map_kv, h * 4 + 3, y);
+        values(0);
+        if (n_tiles > 1) keys(1);
+        for (int i = 1; ok && i < n_tiles; ++i) {
+          values(i);
+          if (ok && i + 1 < n_tiles) keys(i + 1);
         }
         if (!ok) {      // let the copies in flight land before the block ends
           bool landed = true;
           for (int a = 0; a < (two ? 2 : 1); ++a) landed = landed && mbar_wait(&ax->q_full[a], 0, p.budget);
-          for (int i = max(0, n - kSlots); landed && i < n; ++i)
-            landed = mbar_wait(&ax->full[i % kSlots], (i / kSlots) & 1, p.budget);
+          for (int i = max(0, n_k - 2); landed && i < n_k; ++i)
+            landed = mbar_wait(&ax->k_full[i & 1], (i >> 1) & 1, p.budget);
+          for (int i = max(0, n_v - 2); landed && i < n_v; ++i)
+            landed = mbar_wait(&ax->v_full[i & 1], (i >> 1) & 1, p.budget);
         }
       }
     } else if (warp == 1) {
       // ---------------------------------------------------------------- MMAs --
+      // One thread for both row tiles, in a fixed order that keeps them half a
+      // period apart: with a thread each they fall into step, both softmaxes
+      // and then both products (8K at 16 heads 420 -> 502 us).
       if (elect_one()) {
         constexpr uint32_t idesc_s = idesc_f32acc(kFmtBF16, kFmtBF16, 128, 128, 0, 0);
         constexpr uint32_t idesc_o = idesc_f32acc(kFmtBF16, kFmtBF16, 128, 128, 0, 1);     // V MN-major
-        const uint32_t q_addr = smem_u32(sm + OFF_Q), kv_addr = smem_u32(sm + OFF_KV);
+        constexpr uint32_t idesc_half = idesc_f32acc(kFmtBF16, kFmtBF16, 128, 64, 0, 1);
+        // descriptors: offsets are added to the address field (16-byte units)
+        const uint64_t q_desc = smem_desc(smem_u32(sm + OFF_Q), 16, 1024, kSwizzle128B);
+        const uint64_t k_desc = smem_desc(smem_u32(sm + OFF_KV), 16, 1024, kSwizzle128B);
+        const uint64_t v_desc = smem_desc(smem_u32(sm + OFF_KV), kBlk, 1024, kSwizzle128B);
         bool ok = true;
         auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t site) {
           if (ok && !mbar_wait(bar, parity, p.budget)) {
@@ -206,67 +218,65 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           return ok;
         };
-        auto scores = [&](int a, int i) {
-          const bool last = a == 1 || !two;        // of the row tiles that read key tile i
+        // `last`: of the row tiles that read key tile i
+        auto scores = [&](int a, int i, bool last) {
+          const uint32_t d_s = tmem + TM_S + 128 * a;
+          const uint64_t qd = q_desc + a * ((3 * kBlk) >> 4);
+#pragma unroll
           for (int c = 0; c < 3; ++c) {
-            const int n = 5 * i + c, s = n % kSlots;
-            if (!wait(&ax->full[s], (n / kSlots) & 1, 621)) return;
-            tc_fence_after();
+            const uint64_t kd = k_desc + ring(5 * i + c) * (kBlk >> 4);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              umma_f16_ss(tmem + TM_S + 128 * a, smem_desc(q_addr + (3 * a + c) * kBlk + kk * 32, 16, 1024, kSwizzle128B),
-                          smem_desc(kv_addr + s * kBlk + kk * 32, 16, 1024, kSwizzle128B), idesc_s, (c | kk) ? 1u : 0u);
-            if (last) umma_commit(&ax->empty[s]);
+              umma_f16_ss(d_s, qd + ((c * kBlk + kk * 32) >> 4), kd + ((kk * 32) >> 4), idesc_s, (c | kk) ? 1u : 0u);
           }
           umma_commit(&ax->s_full[a]);
-          if (last && i >= border0) {
-            for (int c = 0; c < 2; ++c) {
-              const int n = 5 * i + 3 + c;
-              if (!wait(&ax->full[n % kSlots], (n / kSlots) & 1, 625)) return;
-            }
-            mbar_arrive(&ax->go);
-          }
+          if (last) umma_commit(&ax->k_empty[i & 1]);
         };
-        auto values = [&](int a, int i) {
-          const bool last = a == 1 || !two;
-          if (!wait(&ax->p_full[a], i & 1, 622)) return;
-          if (i >= border0 && !wait(&ax->clean, (i - border0) & 1, 623)) return;
-          for (int c = 0; c < 2; ++c) {
-            const int n = 5 * i + 3 + c;
-            if (!wait(&ax->full[n % kSlots], (n / kSlots) & 1, 624)) return;
-          }
-          tc_fence_after();
+        auto values = [&](int a, int i, bool last) {
+          const uint32_t d_s = tmem + TM_S + 128 * a, d_o = tmem + TM_O + 128 * a;
           // one instruction spans both 64-dim blocks where the ring keeps them side by side, else two
-          const int n0 = (5 * i + 3) % kSlots, n1 = (5 * i + 4) % kSlots;
-          const uint32_t step = static_cast<uint32_t>((n1 - n0) * kBlk);
+          const int n0 = ring(5 * i + 3), n1 = ring(5 * i + 4);
+          const uint64_t vd = v_desc + n0 * (kBlk >> 4);
+          if (n1 > n0) {
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk) {
-            const uint32_t acc = (i | kk) ? 1u : 0u;
-            if (n1 > n0) {
-              umma_f16_ts(tmem + TM_O + 128 * a, tmem + TM_S + 128 * a + kk * 8,
-                          smem_desc(kv_addr + n0 * kBlk + kk * 2048, step, 1024, kSwizzle128B), idesc_o, acc);
-            } else {
-              constexpr uint32_t idesc_half = idesc_f32acc(kFmtBF16, kFmtBF16, 128, 64, 0, 1);
-              umma_f16_ts(tmem + TM_O + 128 * a, tmem + TM_S + 128 * a + kk * 8,
-                          smem_desc(kv_addr + n0 * kBlk + kk * 2048, kBlk, 1024, kSwizzle128B), idesc_half, acc);
-              umma_f16_ts(tmem + TM_O + 128 * a + 64, tmem + TM_S + 128 * a + kk * 8,
-                          smem_desc(kv_addr + n1 * kBlk + kk * 2048, kBlk, 1024, kSwizzle128B), idesc_half, acc);
+            for (int kk = 0; kk < 8; ++kk)
+              umma_f16_ts(d_o, d_s + kk * 8, vd + ((kk * 2048) >> 4), idesc_o, (i | kk) ? 1u : 0u);
+          } else {
+            const uint64_t vd1 = v_desc + n1 * (kBlk >> 4);
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk) {
+              umma_f16_ts(d_o, d_s + kk * 8, vd + ((kk * 2048) >> 4), idesc_half, (i | kk) ? 1u : 0u);
+              umma_f16_ts(d_o + 64, d_s + kk * 8, vd1 + ((kk * 2048) >> 4), idesc_half, (i | kk) ? 1u : 0u);
             }
-          }
-          if (last) {
-            umma_commit(&ax->empty[n0]);
-            umma_commit(&ax->empty[n1]);
           }
           umma_commit(&ax->o_done[a]);
+          if (last) umma_commit(&ax->v_empty[i & 1]);
         };
+        if (border0 == 0) mbar_arrive(&ax->go);
         wait(&ax->q_full[0], 0, 620);
-        if (ok) scores(0, 0);
-        if (ok && two && wait(&ax->q_full[1], 0, 620)) scores(1, 0);
+        wait(&ax->k_full[0], 0, 621);
+        tc_fence_after();
+        if (ok) scores(0, 0, !two);
+        if (ok && two && wait(&ax->q_full[1], 0, 620)) {
+          tc_fence_after();
+          scores(1, 0, true);
+        }
         for (int i = 0; ok && i < n_tiles; ++i) {
-          if (i < w.n[0]) values(0, i);
-          if (ok && i + 1 < w.n[0]) scores(0, i + 1);
-          if (ok && i < w.n[1]) values(1, i);
-          if (ok && i + 1 < w.n[1]) scores(1, i + 1);
+          wait(&ax->v_full[i & 1], (i >> 1) & 1, 624);
+          if (i + 1 == border0) mbar_arrive(&ax->go);
+          if (i >= border0) wait(&ax->clean, (i - border0) & 1, 623);
+#pragma unroll
+          for (int a = 0; a < 2; ++a) {
+            const bool last = a == 1 || !two;
+            if (i >= w.n[a]) continue;
+            if (!wait(&ax->p_full[a], i & 1, 622)) break;
+            tc_fence_after();
+            values(a, i, last);
+            if (i + 1 < w.n[a] && wait(&ax->k_full[(i + 1) & 1], ((i + 1) >> 1) & 1, 625)) {
+              tc_fence_after();
+              scores(a, i + 1, last);
+            }
+          }
         }
       }
     } else {
@@ -279,39 +289,53 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         ok = __all_sync(0xffffffffu, ok);
       };
+      // These warps skip the tiles before the border, and a parity alone would not
+      // tell them where the ring is: the MMA thread, which follows every phase, does once.
+      if (border0 < n_tiles) wait(&ax->go, 0);
       for (int i = border0; ok && i < n_tiles; ++i) {
-        // The MMA thread, which follows every phase of the ring, tells when: these
-        // warps skip the tiles before, and a parity alone would not tell them.
-        wait(&ax->go, (i - border0) & 1);
-        for (int c = 0; ok && c < 2; ++c) {
-          const int n = 5 * i + 3 + c, s = n % kSlots;
-          wait(&ax->full[s], (n / kSlots) & 1);
-          if (!ok) break;
+        wait(&ax->v_full[i & 1], (i >> 1) & 1);
+        if (!ok) break;
+        const int first = max(0, w.base + 1 - i * kKeys);          // the rows before are seen by every row
+        const int dead = w.base + w.rows - i * kKeys;              // rows from here on by none
+#pragma unroll 1
+        for (int c = 0; c < 2; ++c) {
+          uint4* blk = reinterpret_cast<uint4*>(sm + OFF_KV + ring(5 * i + 3 + c) * kBlk);
           // row r of the block is position i * 128 + r; unit u of it holds dims 8 (u ^ (r & 7)) ..
-          for (int u = tid - 64; u < kBlk / 16; u += 64) {
-            const int r = u >> 3, pos = i * kKeys + r;
-            if (pos <= w.base) continue;                       // every row sees it
-            uint4* at = reinterpret_cast<uint4*>(sm + OFF_KV + s * kBlk) + u;
-            if (pos > w.base + w.rows - 1) {                   // no row sees it
-              *at = make_uint4(0, 0, 0, 0);
-              continue;
-            }
-            const uint4 v = *at;
-            uint32_t x[4] = {v.x, v.y, v.z, v.w};
-            bool hit = false;
+#pragma unroll 1
+          for (int u0 = 8 * first + tid - 64; u0 < kBlk / 16; u0 += 4 * 64) {
+            uint4 v[4];
+            bool odd = false;      // a row that no row sees, or a value that is not finite
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const uint32_t mask = 0x7F80u << (16 * (e & 1));
-              if ((x[e >> 1] & mask) == mask) {
-                x[e >> 1] &= 0xFFFFu << (16 * ((e & 1) ^ 1));
-                atomicMin(&ax->bad_pos[c * 64 + 8 * ((u & 7) ^ (r & 7)) + e], pos);
-                hit = true;
+            for (int q = 0; q < 4; ++q) {
+              const int u = u0 + 64 * q;
+              v[q] = u < kBlk / 16 ? blk[u] : make_uint4(0, 0, 0, 0);
+              // an exponent of all ones carries into its half's top bit
+              uint32_t t = 0;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) t |= ((&v[q].x)[e] & 0x7F807F80u) + 0x00800080u;
+              odd |= (t & 0x80008000u) != 0 || (u >> 3) >= dead;
+            }
+            if (!odd) continue;
+#pragma unroll 1
+            for (int q = 0; q < 4; ++q) {
+              const int u = u0 + 64 * q, r = u >> 3;
+              if (u >= kBlk / 16) break;
+              if (r >= dead) {
+                blk[u] = make_uint4(0, 0, 0, 0);
+                continue;
+              }
+              const uint4 a = blk[u];
+              const uint32_t x[4] = {a.x, a.y, a.z, a.w};
+              blk[u] = make_uint4(finite_or_zero(a.x), finite_or_zero(a.y), finite_or_zero(a.z), finite_or_zero(a.w));
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const uint32_t mask = 0x7F80u << (16 * (e & 1));
+                if ((x[e >> 1] & mask) == mask)
+                  atomicMin(&ax->bad_pos[c * 64 + 8 * ((u & 7) ^ (r & 7)) + e], i * kKeys + r);
               }
             }
-            if (hit) *at = make_uint4(x[0], x[1], x[2], x[3]);
           }
         }
-        if (!ok) break;
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&ax->clean);
