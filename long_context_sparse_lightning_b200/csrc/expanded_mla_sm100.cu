@@ -61,6 +61,54 @@ using dense::kGrow;
 using dense::kLn2;
 using dense::pack_bf16;
 
+// f32x2 register pairs (low element first)
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 split(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
+// 2^x of two values on the FMA pipe: x = n + f with n an integer and |f| <= 1/2
+// (adding 1.5 * 2^23 rounds to n and leaves it in the low bits), 2^f by a degree-4
+// polynomial fitted for the smallest relative error on that range (2.7e-6 in fp32, far
+// below the rounding to bf16), n added to the exponent.  -125 <= x: what is smaller
+// gives 2^-125, so masked scores do not come here.
+__device__ __forceinline__ float2 exp2_poly(uint64_t x2) {
+  const float2 xv = split(x2);
+  const uint64_t x = pair(max_nan(xv.x, -125.f), max_nan(xv.y, -125.f));
+  const uint64_t big = pair(12582912.f, 12582912.f), minus = pair(-12582912.f, -12582912.f);
+  const uint64_t y = add2(x, big);
+  const uint64_t n = add2(y, minus);
+  const uint64_t f = fma2(n, pair(-1.f, -1.f), x);
+  uint64_t q = fma2(f, pair(0.009570101276040077f, 0.009570101276040077f), pair(0.05591786280274391f, 0.05591786280274391f));
+  q = fma2(q, f, pair(0.240247443318367f, 0.240247443318367f));
+  q = fma2(q, f, pair(0.6931217908859253f, 0.6931217908859253f));
+  q = fma2(q, f, pair(0.9999992847442627f, 0.9999992847442627f));
+  const float2 qv = split(q), yv = split(y);
+  return make_float2(__int_as_float(__float_as_int(qv.x) + (__float_as_int(yv.x) << 23)),
+                     __int_as_float(__float_as_int(qv.y) + (__float_as_int(yv.y) << 23)));
+}
+
 // What a CTA works on.
 struct Tile {
   int row0, rows;          // rows of q
@@ -379,18 +427,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int j = 0; j < 32; ++j)
             if (32 * c + j > left) s[c][j] = __float_as_uint(NEG_INF);
       }
+      // The row's maximum, NaN if any score is: such a row is NaN from here on.
       float mx[4];
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         mx[c] = __uint_as_float(s[c][0]);
 #pragma unroll
-        for (int j = 1; j < 32; ++j) mx[c] = fmaxf(mx[c], __uint_as_float(s[c][j]));
+        for (int j = 1; j < 32; ++j) mx[c] = max_nan(mx[c], __uint_as_float(s[c][j]));
       }
-      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
-      const bool grow = top > m + kGrow;         // true on the first tile that shows the row a key
+      const float top = max_nan(max_nan(mx[0], mx[1]), max_nan(mx[2], mx[3])) * scale;
+      const bool grow = !(top <= m + kGrow);     // true on the first tile that shows the row a key
       if (__any_sync(0xffffffffu, grow)) {
         const float f = grow ? exp2_approx(m - top) : 1.f;
-        if (grow) m = top;
+        if (grow) m = top < __int_as_float(0x7f800000) ? top : __int_as_float(0x7fffffff);      // an infinite score: NaN too
         l *= f;
         if (i > 0) {
           if (!wait(&ax->o_done[a], (i - 1) & 1, 642)) break;
@@ -412,20 +461,37 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       const float ref = m == NEG_INF ? 0.f : -m;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
+      const uint64_t scale2 = pair(scale, scale), ref2 = pair(ref, ref);
+      uint64_t sum2 = pair(0.f, 0.f);
+      const bool masked = warp_lim - i * kKeys < kKeys - 1;
+      // Some of the exponentials go to the FMA pipe: the two row tiles' 32K at 16 a
+      // cycle would alone take 2048 cycles of a period.
+      auto probabilities = [&](int c, bool poly) {
         uint32_t pk[16];
-        float sum = 0.f;
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
-          const float x = exp2_approx(fmaf(__uint_as_float(s[c][2 * j]), scale, ref));
-          const float y = exp2_approx(fmaf(__uint_as_float(s[c][2 * j + 1]), scale, ref));
-          sum += x + y;
-          pk[j] = pack_bf16(x, y);
+          const uint64_t x = fma2(pair(__uint_as_float(s[c][2 * j]), __uint_as_float(s[c][2 * j + 1])), scale2, ref2);
+          float2 e;
+          if (poly && (j & 3) == 3) {
+            e = exp2_poly(x);
+          } else {
+            const float2 v = split(x);
+            e = make_float2(exp2_approx(v.x), exp2_approx(v.y));
+          }
+          sum2 = add2(sum2, pair(e.x, e.y));
+          pk[j] = pack_bf16(e.x, e.y);
         }
-        l += sum;
         tmem_st16(tS + 16 * c, pk);
+      };
+      if (masked) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) probabilities(c, false);
+      } else {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) probabilities(c, true);
       }
+      const float2 sums = split(sum2);
+      l += sums.x + sums.y;
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
