@@ -48,6 +48,16 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+// 32 bytes to a 16-byte aligned address.
+__device__ __forceinline__ void store_32(void* dst, const uint32_t (&v)[8]) {
+  if ((reinterpret_cast<uintptr_t>(dst) & 31u) == 0) {
+    st_global_32(dst, v);
+  } else {
+    reinterpret_cast<uint4*>(dst)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<uint4*>(dst)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+  }
+}
+
 // Barrier `id` of `threads` threads; the first returns the OR of `v` over them.
 __device__ __forceinline__ bool bar_any(bool v, uint32_t id, uint32_t threads) {
   uint32_t r;

@@ -81,16 +81,6 @@ struct Aux {
 };
 static_assert(sizeof(Aux) <= 2048, "");
 
-// 32 bytes to a 16-byte aligned address.
-__device__ __forceinline__ void store_32(void* dst, const uint32_t (&v)[8]) {
-  if ((reinterpret_cast<uintptr_t>(dst) & 31u) == 0) {
-    st_global_32(dst, v);
-  } else {
-    reinterpret_cast<uint4*>(dst)[0] = make_uint4(v[0], v[1], v[2], v[3]);
-    reinterpret_cast<uint4*>(dst)[1] = make_uint4(v[4], v[5], v[6], v[7]);
-  }
-}
-
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     dense_pair_kernel(const DenseMlaParams p, const __grid_constant__ DenseMaps maps) {
   extern __shared__ uint8_t smem_raw[];

@@ -51,6 +51,7 @@ struct Aux {
   uint64_t s_full[2], p_full[2], o_done[2];
   uint64_t go, clean;       // the values before the border have landed / a border tile's are clean
   uint32_t tmem;
+  int32_t any_bad;
   int32_t bad_pos[128];     // first position whose value of this dim is not finite, per dim
 };
 static_assert(sizeof(Aux) <= 1024, "");
@@ -60,6 +61,7 @@ using dense::finite_or_zero;
 using dense::kGrow;
 using dense::kLn2;
 using dense::pack_bf16;
+using dense::store_32;
 
 // f32x2 register pairs (low element first)
 __device__ __forceinline__ uint64_t pair(float lo, float hi) {
@@ -181,6 +183,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefetch_tmap(&map_r);
   }
   if (tid < 128) ax->bad_pos[tid] = 0x7fffffff;
+  if (tid == 0) ax->any_bad = 0;
   if (warp == 1) {
     tmem_alloc(&ax->tmem, kTmemCols);
     tmem_relinquish();
@@ -343,43 +346,39 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = border0; ok && i < n_tiles; ++i) {
         wait(&ax->v_full[i & 1], (i >> 1) & 1);
         if (!ok) break;
-        const int first = max(0, w.base + 1 - i * kKeys);          // the rows before are seen by every row
-        const int dead = w.base + w.rows - i * kKeys;              // rows from here on by none
+        const int first = max(0, w.base + 1 - i * kKeys);               // the rows before are seen by every row
+        const int dead = min(kKeys, w.base + w.rows - i * kKeys);       // rows from here on by none
 #pragma unroll 1
         for (int c = 0; c < 2; ++c) {
           uint4* blk = reinterpret_cast<uint4*>(sm + OFF_KV + ring(5 * i + 3 + c) * kBlk);
+          for (int u = 8 * max(first, dead) + tid - 64; u < kBlk / 16; u += 64) blk[u] = make_uint4(0, 0, 0, 0);
           // row r of the block is position i * 128 + r; unit u of it holds dims 8 (u ^ (r & 7)) ..
 #pragma unroll 1
-          for (int u0 = 8 * first + tid - 64; u0 < kBlk / 16; u0 += 4 * 64) {
+          for (int u0 = 8 * first + tid - 64; u0 < 8 * dead; u0 += 4 * 64) {
             uint4 v[4];
-            bool odd = false;      // a row that no row sees, or a value that is not finite
+            uint32_t t = 0;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const int u = u0 + 64 * q;
-              v[q] = u < kBlk / 16 ? blk[u] : make_uint4(0, 0, 0, 0);
-              // an exponent of all ones carries into its half's top bit
-              uint32_t t = 0;
+            for (int q = 0; q < 4; ++q) v[q] = u0 + 64 * q < 8 * dead ? blk[u0 + 64 * q] : make_uint4(0, 0, 0, 0);
+            // an exponent of all ones carries into its half's top bit
 #pragma unroll
-              for (int e = 0; e < 4; ++e) t |= ((&v[q].x)[e] & 0x7F807F80u) + 0x00800080u;
-              odd |= (t & 0x80008000u) != 0 || (u >> 3) >= dead;
-            }
-            if (!odd) continue;
+            for (int q = 0; q < 4; ++q)
+              t |= ((v[q].x & 0x7F807F80u) + 0x00800080u) | ((v[q].y & 0x7F807F80u) + 0x00800080u) |
+                   ((v[q].z & 0x7F807F80u) + 0x00800080u) | ((v[q].w & 0x7F807F80u) + 0x00800080u);
+            if ((t & 0x80008000u) == 0) continue;
 #pragma unroll 1
             for (int q = 0; q < 4; ++q) {
               const int u = u0 + 64 * q, r = u >> 3;
-              if (u >= kBlk / 16) break;
-              if (r >= dead) {
-                blk[u] = make_uint4(0, 0, 0, 0);
-                continue;
-              }
+              if (u >= 8 * dead) break;
               const uint4 a = blk[u];
               const uint32_t x[4] = {a.x, a.y, a.z, a.w};
               blk[u] = make_uint4(finite_or_zero(a.x), finite_or_zero(a.y), finite_or_zero(a.z), finite_or_zero(a.w));
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
                 const uint32_t mask = 0x7F80u << (16 * (e & 1));
-                if ((x[e >> 1] & mask) == mask)
+                if ((x[e >> 1] & mask) == mask) {
                   atomicMin(&ax->bad_pos[c * 64 + 8 * ((u & 7) ^ (r & 7)) + e], i * kKeys + r);
+                  ax->any_bad = 1;
+                }
               }
             }
           }
@@ -502,24 +501,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float inv = 1.f / l;
       const int64_t at = static_cast<int64_t>(w.row0 + r) * H + h;
 #pragma unroll 1
-      for (int c = 0; c < 4; ++c) {
-        uint32_t o[32];
-        tmem_ld32(tO + 32 * c, o);
+      for (int c = 0; c < 4; c += 2) {
+        uint32_t o[2][32];
+        tmem_ld32(tO + 32 * c, o[0]);
+        tmem_ld32(tO + 32 * c + 32, o[1]);
         tmem_ld_wait();
+        if (ax->any_bad != 0) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
-          if (ax->bad_pos[32 * c + j] <= lim) o[j] = 0x7FFFFFFFu;
+          for (int j = 0; j < 64; ++j)
+            if (ax->bad_pos[32 * c + j] <= lim) o[j >> 5][j & 31] = 0x7FFFFFFFu;
+        }
         if (r < w.rows) {
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
-            uint4 v;
-            v.x = pack_bf16(__uint_as_float(o[8 * u]) * inv, __uint_as_float(o[8 * u + 1]) * inv);
-            v.y = pack_bf16(__uint_as_float(o[8 * u + 2]) * inv, __uint_as_float(o[8 * u + 3]) * inv);
-            v.z = pack_bf16(__uint_as_float(o[8 * u + 4]) * inv, __uint_as_float(o[8 * u + 5]) * inv);
-            v.w = pack_bf16(__uint_as_float(o[8 * u + 6]) * inv, __uint_as_float(o[8 * u + 7]) * inv);
-            *reinterpret_cast<uint4*>(p.out + at * 128 + 32 * c + 8 * u) = v;
+            const uint32_t* x = &o[u >> 1][16 * (u & 1)];
+            uint32_t v[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              v[e] = pack_bf16(__uint_as_float(x[2 * e]) * inv, __uint_as_float(x[2 * e + 1]) * inv);
+            store_32(p.out + at * 128 + 32 * c + 16 * u, v);
           }
         }
+        __syncwarp();
       }
       if (r < w.rows && p.lse != nullptr) p.lse[at] = (m + log2f(l)) * kLn2;
     }
