@@ -397,7 +397,7 @@ size_t dsa_workspace_size(dsa_op_t op, const dsa_batch_t* batch, int32_t k_sel, 
     case DSA_OP_PREFIX_MLA:
       return dsa::dense_ws_bytes(batch, n_heads, true);
     case DSA_OP_EXPANDED_MLA:
-      return n_heads < 1 || n_heads > 128 ? 0 : kHeaderBytes;
+      return dsa::expanded_ws_bytes(batch, n_heads);
     case DSA_OP_INDEXER_TOPK:
       if (k_sel < 1 || k_sel > DSA_MAX_K_SEL) return 0;
       if (fused_cluster(batch) > 0) return kHeaderBytes;

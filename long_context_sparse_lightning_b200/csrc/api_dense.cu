@@ -36,6 +36,22 @@ DenseLayout dense_layout(const dsa_batch_t* b, int n_heads, bool shared) {
   return l;
 }
 
+// The same of the expanded form: partial results where the keys are split.
+struct ExpandedLayout {
+  int splits;
+  size_t part_lse, part_o, bytes;
+};
+
+ExpandedLayout expanded_layout(const dsa_batch_t* b, int n_heads) {
+  ExpandedLayout l;
+  l.splits = dsa::expanded_splits(b, n_heads);
+  const size_t rows = l.splits > 1 ? static_cast<size_t>(l.splits) * b->total_q * n_heads : 0;
+  l.part_lse = kHeader;
+  l.part_o = l.part_lse + round_up(rows * sizeof(float), 256);
+  l.bytes = l.part_o + rows * 128 * sizeof(float);
+  return l;
+}
+
 dsa_status_t run_dense(const dsa_batch_t* b, int prefix_len, const void* q, int n_heads, const void* kv, float sm_scale,
                        void* out, float* lse, void* ws, size_t ws_bytes, cudaStream_t stream) {
   const bool shared = prefix_len >= 0;
@@ -95,6 +111,11 @@ size_t dense_ws_bytes(const dsa_batch_t* b, int n_heads, bool shared) {
   if (shared && b->block_table == nullptr) return 0;
   return dense_layout(b, n_heads, shared).bytes;
 }
+
+size_t expanded_ws_bytes(const dsa_batch_t* b, int n_heads) {
+  if (n_heads < 1 || n_heads > 128 || b->block_table != nullptr) return 0;
+  return expanded_layout(b, n_heads).bytes;
+}
 }  // namespace dsa
 
 extern "C" {
@@ -123,9 +144,13 @@ dsa_status_t dsa_expanded_mla(const dsa_batch_t* b, const void* q, int32_t n_hea
   if (!(sm_scale > 0.f) || !std::isfinite(sm_scale)) return DSA_ERR_INVALID_ARG;
   if (n_heads < 1 || n_heads > 128 || b->block_table != nullptr) return DSA_ERR_UNSUPPORTED;
   if (ws == nullptr || misaligned(ws, 16)) return DSA_ERR_INVALID_ARG;
-  if (ws_bytes < kHeader) return DSA_ERR_WORKSPACE;
+  const ExpandedLayout l = expanded_layout(b, n_heads);
+  if (ws_bytes < l.bytes) return DSA_ERR_WORKSPACE;
   if (b->total_q == 0) return DSA_OK;
   dsa::ExpandedMlaParams p;
+  p.splits = l.splits;
+  p.part_lse = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + l.part_lse);
+  p.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + l.part_o);
   p.cu_q = b->cu_q;
   p.kv_len = b->kv_len;
   p.kv_start = b->kv_start;

@@ -19,6 +19,9 @@
 // Roles: warp 0 TMA, warp 1 MMAs of both tiles, warps 2-3 clean the value
 // tiles on the border (below), warps 4-7 and 8-11 softmax and epilogue of the tiles.
 //
+// Few rows over long contexts: the key tiles are split over several CTAs, whose
+// normalised fp32 results and log-sum-exps expanded_merge_kernel joins.
+//
 // A position that some row of the CTA must not see has probability 0 there,
 // and 0 x a non-finite value would reach that row all the same.  So in tiles on
 // the border the cleaning warps zero the value rows that no row of the CTA
@@ -34,8 +37,9 @@ constexpr int kKeys = 128;                 // keys per tile
 constexpr int kBlk = 128 * 128;            // one [128 rows x 64 dims] block, 128-byte swizzle
 constexpr int kSlots = 8;                  // ring of key / value blocks, 3 + 2 per tile
 __device__ __forceinline__ int ring(int block) { return block & (kSlots - 1); }
+constexpr int kSplitTiles = 3;             // key tiles a part of a split has at least
 constexpr int kThreads = 12 * 32;
-constexpr uint32_t kRegLow = 88, kRegHigh = 208;     // 128 * (88 + 2 * 208) = 384 * 168
+constexpr uint32_t kRegLow = 120, kRegHigh = 192;    // 128 * (120 + 2 * 192) = 384 * 168
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t TM_S = 0, TM_O = 256;   // + 128 * tile
 
@@ -114,16 +118,18 @@ __device__ __forceinline__ float2 exp2_poly(uint64_t x2) {
 // What a CTA works on.
 struct Tile {
   int row0, rows;          // rows of q
-  int base;                // position of row 0
-  int n[2];                // key tiles of the two row tiles (0: no rows)
-  int first_row_key;       // cache row of position 0
+  int base;                // position of row 0, counted from the CTA's first key
+  int n[2];                // key tiles of the two row tiles (0: nothing to do)
+  int first_row_key;       // cache row of the first key
   bool bad;
 };
 
+template <bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
     expanded_mla_kernel(const ExpandedMlaParams p, const __grid_constant__ CUtensorMap map_q,
                         const __grid_constant__ CUtensorMap map_kv, const __grid_constant__ CUtensorMap map_r) {
-  const int b = blockIdx.z, h = blockIdx.y;
+  const int part = SPLIT ? static_cast<int>(blockIdx.z) % p.splits : 0;
+  const int b = SPLIT ? static_cast<int>(blockIdx.z) / p.splits : static_cast<int>(blockIdx.z), h = blockIdx.y;
   const int qt = static_cast<int>(gridDim.x) - 1 - static_cast<int>(blockIdx.x);     // the longest rows first
   const int q0 = __ldg(&p.cu_q[b]), q1 = __ldg(&p.cu_q[b + 1]);
   if (q0 < 0 || q1 < q0 || q1 > p.total_q || (b == 0 && q0 != 0)) {
@@ -143,19 +149,31 @@ __global__ void __launch_bounds__(kThreads, 1)
   w.n[1] = w.rows > kRows ? (w.base + w.rows - 1) / kKeys + 1 : 0;
   w.first_row_key = static_cast<int>(ks);
   const int H = p.n_heads, tid = threadIdx.x;
-  if (w.bad) {
-    if (qt == 0 && h == 0 && tid == 0) report_error(p.err, kDevErrBounds, 602, b);
-    for (int u = tid; u < w.rows * 16; u += kThreads)
-      *reinterpret_cast<uint4*>(p.out + (static_cast<int64_t>(w.row0 + (u >> 4)) * H + h) * 128 + (u & 15) * 8) =
-          make_uint4(0, 0, 0, 0);
-    if (p.lse != nullptr)
+  const int64_t part_rows = static_cast<int64_t>(part) * p.total_q;      // this part's rows in the partial results
+  if (SPLIT && !w.bad) {
+    // this CTA's share of the key tiles
+    const int all = max(w.n[0], w.n[1]), per = (all + p.splits - 1) / p.splits, t0 = min(part * per, all);
+    w.n[0] = max(0, min(w.n[0], t0 + per) - t0);
+    w.n[1] = max(0, min(w.n[1], t0 + per) - t0);
+    w.base -= t0 * kKeys;
+    w.first_row_key += t0 * kKeys;
+  }
+  if (w.bad || max(w.n[0], w.n[1]) == 0) {
+    if (w.bad && qt == 0 && h == 0 && part == 0 && tid == 0) report_error(p.err, kDevErrBounds, 602, b);
+    if (!SPLIT) {
+      for (int u = tid; u < w.rows * 16; u += kThreads)
+        *reinterpret_cast<uint4*>(p.out + (static_cast<int64_t>(w.row0 + (u >> 4)) * H + h) * 128 + (u & 15) * 8) =
+            make_uint4(0, 0, 0, 0);
+    }
+    float* lse = SPLIT ? p.part_lse + part_rows * H : p.lse;
+    if (lse != nullptr)
       for (int r = tid; r < w.rows; r += kThreads)
-        p.lse[static_cast<int64_t>(w.row0 + r) * H + h] = __int_as_float(0xff800000);
+        lse[static_cast<int64_t>(w.row0 + r) * H + h] = __int_as_float(0xff800000);
     return;
   }
   const int n_tiles = max(w.n[0], w.n[1]);
   const bool two = w.n[1] > 0;
-  const int border0 = (w.base + 1) / kKeys;      // first tile with a position that row 0 must not see
+  const int border0 = w.base < 0 ? 0 : (w.base + 1) / kKeys;      // first tile with a position that row 0 must not see
 
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -306,12 +324,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (border0 == 0) mbar_arrive(&ax->go);
         wait(&ax->q_full[0], 0, 620);
         wait(&ax->k_full[0], 0, 621);
+        if (two) wait(&ax->q_full[1], 0, 620);
         tc_fence_after();
-        if (ok) scores(0, 0, !two);
-        if (ok && two && wait(&ax->q_full[1], 0, 620)) {
-          tc_fence_after();
-          scores(1, 0, true);
-        }
+        if (ok && w.n[0] > 0) scores(0, 0, !two);
+        if (ok && two) scores(1, 0, true);
         for (int i = 0; ok && i < n_tiles; ++i) {
           wait(&ax->v_full[i & 1], (i >> 1) & 1, 624);
           if (i + 1 == border0) mbar_arrive(&ax->go);
@@ -498,7 +514,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (ok && nt > 0 && wait(&ax->o_done[a], (nt - 1) & 1, 643)) {
       tc_fence_after();
-      const float inv = 1.f / l;
+      const float inv = l == 0.f ? 0.f : 1.f / l;      // 0: a part of the keys that the row does not see
       const int64_t at = static_cast<int64_t>(w.row0 + r) * H + h;
 #pragma unroll 1
       for (int c = 0; c < 4; c += 2) {
@@ -511,7 +527,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int j = 0; j < 64; ++j)
             if (ax->bad_pos[32 * c + j] <= lim) o[j >> 5][j & 31] = 0x7FFFFFFFu;
         }
-        if (r < w.rows) {
+        if (SPLIT && r < w.rows) {
+          float* to = p.part_o + (part_rows * H + at) * 128 + 32 * c;
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            uint32_t v[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = __float_as_uint(__uint_as_float(o[u >> 2][8 * (u & 3) + e]) * inv);
+            store_32(to + 8 * u, v);
+          }
+        } else if (r < w.rows) {
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
             const uint32_t* x = &o[u >> 1][16 * (u & 1)];
@@ -524,7 +549,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
       }
-      if (r < w.rows && p.lse != nullptr) p.lse[at] = (m + log2f(l)) * kLn2;
+      if (r < w.rows) {
+        const float lse2 = l == 0.f ? NEG_INF : m + log2f(l);
+        if (SPLIT) {
+          p.part_lse[part_rows * H + at] = lse2;
+        } else if (p.lse != nullptr) {
+          p.lse[at] = lse2 * kLn2;
+        }
+      }
+    } else if (SPLIT && nt == 0 && r < w.rows) {
+      p.part_lse[part_rows * H + static_cast<int64_t>(w.row0 + r) * H + h] = NEG_INF;
     }
   }
   tc_fence_before();
@@ -535,14 +569,62 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+// Joins the parts of each (row, head), a warp each, 4 dims a lane: weights 2^(lse_i - max).
+__global__ void __launch_bounds__(256) expanded_merge_kernel(const ExpandedMlaParams p) {
+  const float NEG_INF = __int_as_float(0xff800000);
+  const int64_t all = static_cast<int64_t>(p.total_q) * p.n_heads;
+  const int64_t rows = static_cast<int64_t>(min(max(__ldg(&p.cu_q[p.num_seqs]), 0), p.total_q)) * p.n_heads;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  const int lane = static_cast<int>(threadIdx.x & 31u);
+  if (row >= rows) return;
+  float m = NEG_INF;
+  for (int i = lane; i < p.splits; i += 32) m = fmaxf(m, p.part_lse[i * all + row]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const float ref = m == NEG_INF ? 0.f : m;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float sum = 0.f;
+#pragma unroll 4
+  for (int i = 0; i < p.splits; ++i) {
+    const float z = p.part_lse[i * all + row];
+    if (z == NEG_INF) continue;            // an empty part: its output was not written
+    const float w = exp2f(z - ref);
+    const float4 v = *reinterpret_cast<const float4*>(p.part_o + (i * all + row) * 128 + lane * 4);
+    sum += w;
+    acc.x += w * v.x;
+    acc.y += w * v.y;
+    acc.z += w * v.z;
+    acc.w += w * v.w;
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  uint2 out;
+  out.x = pack_bf16(acc.x * inv, acc.y * inv);
+  out.y = pack_bf16(acc.z * inv, acc.w * inv);
+  *reinterpret_cast<uint2*>(p.out + row * 128 + lane * 4) = out;
+  if (lane == 0 && p.lse != nullptr) p.lse[row] = sum == 0.f ? NEG_INF : (ref + log2f(sum)) * kLn2;
+}
+
 }  // namespace
+
+int expanded_splits(const dsa_batch_t* b, int n_heads) {
+  const int64_t ctas = static_cast<int64_t>((b->max_q_per_seq + 2 * kRows - 1) / (2 * kRows)) * n_heads * b->num_seqs;
+  if (ctas < 1 || ctas > kDenseMaxCtas / 2) return 1;
+  const int tiles = (b->max_kv_len + kKeys - 1) / kKeys;
+  const int64_t s = kDenseMaxCtas / ctas;
+  return static_cast<int>(s < tiles / kSplitTiles ? s : (tiles / kSplitTiles > 1 ? tiles / kSplitTiles : 1));
+}
 
 cudaError_t launch_expanded_mla(const ExpandedMlaParams& p, int max_q_per_seq, const CUtensorMap& map_q,
                                 const CUtensorMap& map_kv, const CUtensorMap& map_r, cudaStream_t stream) {
-  const cudaError_t e = cudaFuncSetAttribute(expanded_mla_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  const auto kernel = p.splits > 1 ? expanded_mla_kernel<true> : expanded_mla_kernel<false>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
-  const dim3 grid((max_q_per_seq + 2 * kRows - 1) / (2 * kRows), p.n_heads, p.num_seqs);
-  expanded_mla_kernel<<<grid, kThreads, kSmem, stream>>>(p, map_q, map_kv, map_r);
+  const dim3 grid((max_q_per_seq + 2 * kRows - 1) / (2 * kRows), p.n_heads, p.num_seqs * p.splits);
+  kernel<<<grid, kThreads, kSmem, stream>>>(p, map_q, map_kv, map_r);
+  const cudaError_t f = cudaGetLastError();
+  if (f != cudaSuccess || p.splits == 1) return f;
+  const int64_t rows = static_cast<int64_t>(p.total_q) * p.n_heads;
+  expanded_merge_kernel<<<static_cast<unsigned>((rows + 7) / 8), 256, 0, stream>>>(p);
   return cudaGetLastError();
 }
 

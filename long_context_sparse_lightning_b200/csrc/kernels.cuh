@@ -59,6 +59,7 @@ __device__ __forceinline__ int64_t cache_row(const PageTable& pt, int b, int64_t
 
 // Workspace bytes of the dense latent attentions (0: arguments the kernels do not take)
 size_t dense_ws_bytes(const dsa_batch_t* b, int n_heads, bool shared);
+size_t expanded_ws_bytes(const dsa_batch_t* b, int n_heads);
 
 // clock64 cycles one bounded device wait may take before it records
 // DSA_ERR_DEVICE_TIMEOUT: DSA_WAIT_BUDGET_CYCLES if set (> 0), else ~1 s
@@ -267,9 +268,14 @@ struct ExpandedMlaParams {
   float scale_log2 = 0.f;             // sm_scale * log2(e)
   uint16_t* out = nullptr;            // bf16 [total_q, H, 128]
   float* lse = nullptr;               // [total_q, H] or nullptr
+  int32_t splits = 1;                 // parts the key tiles of a row tile are split into
+  float* part_lse = nullptr;          // splits > 1: [splits, total_q, H] log2 units
+  float* part_o = nullptr;            // splits > 1: [splits, total_q, H, 128] normalised
   uint32_t* err = nullptr;
   long long budget = 2000000000LL;
 };
+// Parts for a batch: 1 unless its row tiles leave half of the SMs idle.
+int expanded_splits(const dsa_batch_t* b, int n_heads);
 // Descriptors (see make_tmap_blocks) of q as [total_q, H * 192], boxes of 3 x 128;
 // kv_up as [total_keys, H * 256] and the RoPE dims [total_keys, 64], boxes of 1 x 128.
 cudaError_t launch_expanded_mla(const ExpandedMlaParams& p, int max_q_per_seq, const CUtensorMap& map_q,

@@ -49,6 +49,11 @@ CASES = [
     ([100, 300, 1, 513], [100, 333, 513, 640], 4),
     ([64], [2000], 16),
     ([30], [30], 128),
+    # few rows, long contexts: the keys are split
+    ([1], [5000], 2),
+    ([200], [3001], 3),
+    ([256, 7], [2600, 400], 1),                   # parts that end before the other sequence's, or hold none of its keys
+    ([300], [2049], 1),
 ]
 
 
