@@ -239,6 +239,26 @@ class Batch:
                      torch.from_numpy(ks).to(device), int(cu[-1]), int(q_len.max()) if q_len.size else 0,
                      int(kl.max()) if kl.size else 0, int(total_keys))
 
+    @staticmethod
+    def from_requests(q_len: torch.Tensor, kv_before: torch.Tensor, free_pages: torch.Tensor, page_size: int,
+                      block_table: torch.Tensor, ws: torch.Tensor, total_q: int, max_q_per_seq: int, max_kv_len: int,
+                      total_keys: int, stream=None):
+        """A paged step's batch from its requests' lengths, on the device (page_tables): each request has
+        kv_before[b] positions and takes q_len[b] new tokens, whose pages come from free_pages in order and are
+        entered in block_table.  The host sizes may be bounds, as for a captured step: total_q rows are the
+        padded count.  Returns the batch, the rows' positions (indexer_prep's pos) and cache rows, and the
+        number of pages taken (int32 [1])."""
+        device = q_len.device
+        cu_q = torch.empty(q_len.numel() + 1, dtype=torch.int32, device=device)
+        kv_len = torch.empty(q_len.numel(), dtype=torch.int32, device=device)
+        pos = torch.empty(total_q, dtype=torch.int32, device=device)
+        slots = torch.empty(total_q, dtype=torch.int64, device=device)
+        used = torch.empty(1, dtype=torch.int32, device=device)
+        page_tables(q_len, kv_before, free_pages, page_size, block_table, cu_q, kv_len, pos, slots, used, ws, stream)
+        batch = Batch(cu_q, kv_len, None, total_q, max_q_per_seq, max_kv_len, total_keys, block_table=block_table,
+                      page_size=page_size)
+        return batch, pos, slots, used
+
     @property
     def ref(self):
         return ctypes.byref(self.c)

@@ -187,6 +187,8 @@ dsa_status_t dsa_page_tables(int32_t num_seqs, const int32_t* q_len, const int32
       pages_used == nullptr || (free_pages == nullptr && n_free > 0) ||
       ((pos == nullptr || slots == nullptr) && max_tokens > 0))
     return DSA_ERR_INVALID_ARG;
+  // positions and pool rows are int32 in a batch
+  if (static_cast<int64_t>(blocks_per_seq) * page_size >= (int64_t(1) << 31)) return DSA_ERR_UNSUPPORTED;
   struct Range {
     const void* at;
     size_t bytes;
@@ -213,8 +215,6 @@ dsa_status_t dsa_page_tables(int32_t num_seqs, const int32_t* q_len, const int32
     for (const Range& b : out)
       if (&a != &b && overlap(a, b)) return DSA_ERR_INVALID_ARG;
   }
-  // positions and pool rows are int32 in a batch
-  if (static_cast<int64_t>(blocks_per_seq) * page_size >= (int64_t(1) << 31)) return DSA_ERR_UNSUPPORTED;
   if (ws == nullptr || misaligned(ws, 16)) return DSA_ERR_INVALID_ARG;
   if (ws_bytes < kHeader) return DSA_ERR_WORKSPACE;
   dsa::PageTablesParams p;
