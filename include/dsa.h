@@ -301,6 +301,7 @@ DSA_API dsa_status_t dsa_dense_mla(const dsa_batch_t* batch, const void* q, int3
  * batch, whose heads fill whole tiles there; positions from prefix_len on through
  * each sequence's own row.  The result is dsa_dense_mla's of the same batch, up
  * to rounding, where the table rows name equal entries for the prefix.
+ *   Row 0 names the prefix's pages whether or not sequence 0 has tokens.
  *   0 <= prefix_len <= max_kv_len; a sequence with kv_len - q_len < prefix_len
  *   records DSA_ERR_DEVICE_BOUNDS and gets out = 0, lse = -inf.  Flat caches (block_table
  *   == NULL) are DSA_ERR_UNSUPPORTED.  ws of DSA_OP_PREFIX_MLA bytes. */
@@ -321,8 +322,9 @@ DSA_API dsa_status_t dsa_prefix_mla(const dsa_batch_t* batch, int32_t prefix_len
  *   1 <= n_heads <= 128; flat caches only (block_table != NULL is
  *   DSA_ERR_UNSUPPORTED: the expanded rows are made for the call).
  *   ws of DSA_OP_EXPANDED_MLA bytes.
- * Arithmetic, masked positions, rows behind the last sequence and bad descriptors as
- * dsa_dense_mla; a non-finite value that a row does see makes that output NaN. */
+ * Arithmetic, masked positions, rows behind the last sequence and bad descriptors (q_len >
+ * max_q_per_seq among them) as dsa_dense_mla; a non-finite value that a row does
+ * see makes that output NaN. */
 DSA_API dsa_status_t dsa_expanded_mla(const dsa_batch_t* batch, const void* q, int32_t n_heads, const void* kv_up,
                                       const void* rope, int64_t rope_stride, float sm_scale, void* out, float* lse,
                                       void* ws, size_t ws_bytes, dsa_stream_t stream);

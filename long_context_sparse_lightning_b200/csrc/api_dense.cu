@@ -148,6 +148,7 @@ dsa_status_t dsa_expanded_mla(const dsa_batch_t* b, const void* q, int32_t n_hea
   if (ws_bytes < l.bytes) return DSA_ERR_WORKSPACE;
   if (b->total_q == 0) return DSA_OK;
   dsa::ExpandedMlaParams p;
+  p.max_q = b->max_q_per_seq;
   p.splits = l.splits;
   p.part_lse = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + l.part_lse);
   p.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + l.part_o);
@@ -171,7 +172,7 @@ dsa_status_t dsa_expanded_mla(const dsa_batch_t* b, const void* q, int32_t n_hea
       !dsa::make_tmap_blocks(&map_r, rope, static_cast<uint64_t>(b->total_keys), 1, static_cast<uint64_t>(rope_stride),
                              128, 1))
     return DSA_ERR_CUDA;
-  return dsa::launch_expanded_mla(p, b->max_q_per_seq, map_q, map_kv, map_r, reinterpret_cast<cudaStream_t>(stream)) ==
+  return dsa::launch_expanded_mla(p, map_q, map_kv, map_r, reinterpret_cast<cudaStream_t>(stream)) ==
                  cudaSuccess
              ? DSA_OK
              : DSA_ERR_CUDA;

@@ -207,13 +207,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       end.n_tiles = -1;
       publish(end);
     }
-    if (!ok && rank == 0) {
-      // a wait ran out: let the copies in flight (both CTAs') land before the blocks end
-      bool landed = true;
-      if (n_q > 0) landed = mbar_wait(&ax->q_full, (n_q - 1) & 1, p.budget);
-      for (int i = max(0, t - kStages); landed && i < t; ++i)
-        landed = mbar_wait(&ax->full[i % kStages], (i / kStages) & 1, p.budget);
-    }
+    if (!ok) drain_pause();      // a wait ran out: the copies in flight land before the blocks end
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMAs --
     if (rank == 0 && elect_one()) {
@@ -281,6 +275,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         ++n_o;
       }
+      if (!ok) drain_pause();      // the MMAs in flight, before their memory goes
     }
   } else if (warp == 2) {
     // ------------------------- the other CTA's keys at this CTA's dims by TMA --
@@ -322,11 +317,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         __syncwarp();
       }
     }
-    if (!ok) {
-      bool landed = true;
-      for (int i = max(0, n_own - kStages); landed && i < n_own; ++i)
-        landed = mbar_wait(&ax->v_full[i % kStages], (i / kStages) & 1, p.budget);
-    }
+    if (!ok) drain_pause();
   } else if (warp >= 4) {
     // ---------------------------------------------------- softmax, epilogue --
     // The two warpgroups take turns at the tiles: one alone, a warp per scheduler,

@@ -80,6 +80,7 @@ struct Aux {
   uint64_t p_full[2], p_empty[2];
   uint64_t o_full, o_empty;
   uint64_t item_full[2], item_free[2];
+  uint64_t drain;
   Item item[2];
   int32_t skip[10];         // the tile whose first pair has this slot lies on a page outside the pool
   uint32_t tmem;
@@ -149,6 +150,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&ax->item_full[i], 1);
       mbar_init(&ax->item_free[i], 5);      // the MMA thread and the softmax warps
     }
+    mbar_init(&ax->drain, 1);
     mbar_init(&ax->o_full, 1);
     mbar_init(&ax->o_empty, 4);
     fence_mbar_init();
@@ -246,11 +248,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!ok) {
       // a wait ran out: let the copies in flight land before the block ends
       bool landed = true;
-      if (n_q > 0) landed = mbar_wait(&ax->q_full, (n_q - 1) & 1, p.budget) && landed;
+      if (n_q > 0) landed = mbar_wait(&ax->q_full, (n_q - 1) & 1, kDrainCycles) && landed;
       for (int i = max(0, n_rope - C::ROPE_SLOTS); landed && i < n_rope; ++i)
-        landed = mbar_wait(&ax->rope_full[i % C::ROPE_SLOTS], (i / C::ROPE_SLOTS) & 1, p.budget);
+        landed = mbar_wait(&ax->rope_full[i % C::ROPE_SLOTS], (i / C::ROPE_SLOTS) & 1, kDrainCycles);
       for (int i = max(0, n_pair - C::PAIR_SLOTS); landed && i < n_pair; ++i)
-        landed = mbar_wait(&ax->pair_full[i % C::PAIR_SLOTS], (i / C::PAIR_SLOTS) & 1, p.budget);
+        landed = mbar_wait(&ax->pair_full[i % C::PAIR_SLOTS], (i / C::PAIR_SLOTS) & 1, kDrainCycles);
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMAs --
@@ -322,6 +324,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (i + 1 == nt) umma_commit(&ax->o_full);
         }
         ++n_o;
+      }
+      if (!ok) {
+        umma_commit(&ax->drain);
+        mbar_wait(&ax->drain, 0, kDrainCycles);
       }
     }
   } else {

@@ -53,6 +53,7 @@ struct Aux {
   uint64_t q_full[2];
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];      // by tile parity
   uint64_t s_full[2], p_full[2], o_done[2];
+  uint64_t drain;
   uint64_t go, clean;       // the values before the border have landed / a border tile's are clean
   uint32_t tmem;
   int32_t any_bad;
@@ -141,7 +142,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int kv = __ldg(&p.kv_len[b]);
   const int64_t ks = __ldg(&p.kv_start[b]);
   Tile w;
-  w.bad = q_len > kv || kv > p.max_kv_len || ks < 0 || ks + kv > p.total_keys;
+  w.bad = q_len > kv || q_len > p.max_q || kv > p.max_kv_len || ks < 0 || ks + kv > p.total_keys;
   w.row0 = q0 + qt * 2 * kRows;
   w.rows = min(2 * kRows, q_len - qt * 2 * kRows);
   w.base = kv - q_len + qt * 2 * kRows;
@@ -193,6 +194,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&ax->k_empty[i], 1);
       mbar_init(&ax->v_empty[i], 1);
     }
+    mbar_init(&ax->drain, 1);
     mbar_init(&ax->go, 1);
     mbar_init(&ax->clean, 2);
     fence_mbar_init();
@@ -259,11 +261,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!ok) {      // let the copies in flight land before the block ends
           bool landed = true;
-          for (int a = 0; a < (two ? 2 : 1); ++a) landed = landed && mbar_wait(&ax->q_full[a], 0, p.budget);
+          for (int a = 0; a < (two ? 2 : 1); ++a) landed = landed && mbar_wait(&ax->q_full[a], 0, kDrainCycles);
           for (int i = max(0, n_k - 2); landed && i < n_k; ++i)
-            landed = mbar_wait(&ax->k_full[i & 1], (i >> 1) & 1, p.budget);
+            landed = mbar_wait(&ax->k_full[i & 1], (i >> 1) & 1, kDrainCycles);
           for (int i = max(0, n_v - 2); landed && i < n_v; ++i)
-            landed = mbar_wait(&ax->v_full[i & 1], (i >> 1) & 1, p.budget);
+            landed = mbar_wait(&ax->v_full[i & 1], (i >> 1) & 1, kDrainCycles);
         }
       }
     } else if (warp == 1) {
@@ -344,6 +346,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               scores(a, i + 1, last);
             }
           }
+        }
+        if (!ok) {
+          umma_commit(&ax->drain);
+          mbar_wait(&ax->drain, 0, kDrainCycles);
         }
       }
     } else {
@@ -614,12 +620,12 @@ int expanded_splits(const dsa_batch_t* b, int n_heads) {
   return static_cast<int>(s < tiles / kSplitTiles ? s : (tiles / kSplitTiles > 1 ? tiles / kSplitTiles : 1));
 }
 
-cudaError_t launch_expanded_mla(const ExpandedMlaParams& p, int max_q_per_seq, const CUtensorMap& map_q,
-                                const CUtensorMap& map_kv, const CUtensorMap& map_r, cudaStream_t stream) {
+cudaError_t launch_expanded_mla(const ExpandedMlaParams& p, const CUtensorMap& map_q, const CUtensorMap& map_kv,
+                                const CUtensorMap& map_r, cudaStream_t stream) {
   const auto kernel = p.splits > 1 ? expanded_mla_kernel<true> : expanded_mla_kernel<false>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
-  const dim3 grid((max_q_per_seq + 2 * kRows - 1) / (2 * kRows), p.n_heads, p.num_seqs * p.splits);
+  const dim3 grid((p.max_q + 2 * kRows - 1) / (2 * kRows), p.n_heads, p.num_seqs * p.splits);
   kernel<<<grid, kThreads, kSmem, stream>>>(p, map_q, map_kv, map_r);
   const cudaError_t f = cudaGetLastError();
   if (f != cudaSuccess || p.splits == 1) return f;

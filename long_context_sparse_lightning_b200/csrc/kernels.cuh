@@ -268,6 +268,7 @@ struct ExpandedMlaParams {
   float scale_log2 = 0.f;             // sm_scale * log2(e)
   uint16_t* out = nullptr;            // bf16 [total_q, H, 128]
   float* lse = nullptr;               // [total_q, H] or nullptr
+  int32_t max_q = 0;                  // most query tokens of a sequence (the grid's)
   int32_t splits = 1;                 // parts the key tiles of a row tile are split into
   float* part_lse = nullptr;          // splits > 1: [splits, total_q, H] log2 units
   float* part_o = nullptr;            // splits > 1: [splits, total_q, H, 128] normalised
@@ -278,8 +279,8 @@ struct ExpandedMlaParams {
 int expanded_splits(const dsa_batch_t* b, int n_heads);
 // Descriptors (see make_tmap_blocks) of q as [total_q, H * 192], boxes of 3 x 128;
 // kv_up as [total_keys, H * 256] and the RoPE dims [total_keys, 64], boxes of 1 x 128.
-cudaError_t launch_expanded_mla(const ExpandedMlaParams& p, int max_q_per_seq, const CUtensorMap& map_q,
-                                const CUtensorMap& map_kv, const CUtensorMap& map_r, cudaStream_t stream);
+cudaError_t launch_expanded_mla(const ExpandedMlaParams& p, const CUtensorMap& map_q, const CUtensorMap& map_kv,
+                                const CUtensorMap& map_r, cudaStream_t stream);
 
 // ------------------------------------------------------------ page tables --
 struct PageTablesParams {

@@ -137,6 +137,14 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity
   return true;
 }
 
+// After a wait has run out: time for what is still in flight (copies into shared
+// memory, MMAs) to finish before the block ends, whatever the wait budget is.
+constexpr long long kDrainCycles = 1LL << 22;      // ~2 ms, for waits on barriers
+__device__ __forceinline__ void drain_pause() {    // where there is no barrier to wait on: ~0.1 ms
+  const long long t0 = clock64();
+  while (clock64() - t0 < 200000) __nanosleep(1000);
+}
+
 // ----------------------------------------------------------------------------
 // cluster helpers
 // ----------------------------------------------------------------------------

@@ -127,3 +127,17 @@ def test_equals_the_absorbed_form():
     # per form: the operands' rounding (keys, values or absorbed q: 2^-8 each, which moves a score of size
     # |q||k| scale ~ 1 by as much), the probabilities' and the output's: six half steps in all, in the 2-norm
     assert (out.cpu().double() - o2).norm() <= 6 * 2.0 ** -8 * o2.norm()
+
+
+def test_more_tokens_than_the_host_said_is_a_bounds_error():
+    c = Expanded([300, 10], [300, 40], 1, seed=7)
+    want = c.exact_expanded()
+    c.batch.c.max_q_per_seq = 256                    # sizes the grid: sequence 0's last rows have no block
+    out, lse = c.outputs(128)
+    ws = dsa.workspace(dsa.OP_EXPANDED_MLA, c.batch, n_heads=1)
+    dsa.expanded_mla(c.batch, c.q.cuda(), c.up.cuda(), c.cache.cuda()[:, 512:], c.scale, out, lse, ws)
+    with pytest.raises(dsa.DSAError) as e:
+        dsa.check_device_error(ws)
+    assert e.value.status == 6
+    assert (out[:256] == 0).all() and torch.isneginf(lse[:256]).all()
+    assert (out[300:310].cpu().double() - want[0][300:]).norm() <= 2.0 ** -8 * want[0][300:].norm()
