@@ -729,7 +729,7 @@ cudaError_t launch_dense_mla(const DenseMlaParams& p, const DensePlan& d, const 
   }
   if (e != cudaSuccess) return e;
   const int64_t rows = static_cast<int64_t>(p.total_q) * p.n_heads;
-  const bool few = rows <= 4 * 148;
+  const bool few = rows <= 8 * 148;
   const int64_t blocks = few ? rows : (rows + 7) / 8;
   const int grid = static_cast<int>(blocks < 148 * 8 ? blocks : 148 * 8);
   if (few) {
