@@ -230,6 +230,8 @@ dsa_status_t dsa_page_tables(int32_t num_seqs, const int32_t* q_len, const int32
   p.used = pages_used;
   p.num_seqs = num_seqs;
   p.page = page_size;
+  if ((page_size & (page_size - 1)) == 0)
+    for (p.page_shift = 0; (1 << p.page_shift) < page_size;) ++p.page_shift;
   p.blocks = blocks_per_seq;
   p.n_free = n_free;
   p.max_tokens = max_tokens;

@@ -297,6 +297,7 @@ struct PageTablesParams {
   int32_t* used = nullptr;
   int32_t num_seqs = 0;
   int32_t page = 0;
+  int32_t page_shift = -1;            // log2 of page, -1: not a power of two
   int32_t blocks = 0;
   int32_t n_free = 0;
   int32_t max_tokens = 0;

@@ -16,7 +16,12 @@ namespace dsa {
 namespace {
 
 constexpr int kSeqs = 256;       // sequences (and threads) per block
-constexpr int kTokens = 4096;    // tokens a block walks before the walk is split further
+constexpr int kTokens = 512;     // tokens a block walks before the walk is split further (4096: 10.3 against 5 us for 33K tokens)
+
+// x / page: a shift where the page size is a power of two
+__device__ __forceinline__ int page_of(const PageTablesParams& p, int x) {
+  return p.page_shift >= 0 ? x >> p.page_shift : x / p.page;
+}
 
 struct SeqPages {
   int q, before, have, need, bad;
@@ -139,13 +144,13 @@ __global__ void __launch_bounds__(kSeqs) page_tables_kernel(const PageTablesPara
   for (long long r = tok[0] + at; r < end; r += step) {
     const int i = find(tok, n, r);
     const int pos = before_s[i] + static_cast<int>(r - tok[i]);
-    const int blk = pos / p.page;
+    const int blk = page_of(p, pos);
     // an entry held before the call, or one that this call takes (no other block's write is read)
     const int id = blk < have_s[i] ? p.block_table[static_cast<int64_t>(b0 + i) * p.blocks + blk]
                                    : page_at(pg[i] + blk - have_s[i]);
     if (id < 0) report_error(p.err, kDevErrBounds, 704, b0 + i);
     p.pos[r] = pos;
-    p.slots[r] = id < 0 ? -1 : static_cast<int64_t>(id) * p.page + pos % p.page;
+    p.slots[r] = id < 0 ? -1 : static_cast<int64_t>(id) * p.page + (pos - blk * p.page);
   }
   if (last) {
     for (long long r = end + at; r < p.max_tokens; r += step) {
@@ -159,9 +164,10 @@ __global__ void __launch_bounds__(kSeqs) page_tables_kernel(const PageTablesPara
 
 cudaError_t launch_page_tables(const PageTablesParams& p, cudaStream_t stream) {
   const int nx = (p.num_seqs + kSeqs - 1) / kSeqs;
-  // one pass of the walk over max_tokens, split while the blocks fit one wave
+  // the walk over max_tokens, split while there are at most two blocks per SM
   int ny = (p.max_tokens + kTokens - 1) / kTokens;
-  ny = ny < 1 ? 1 : (ny > 64 ? 64 : ny);
+  const int most = nx < 2 * sm_count() ? 2 * sm_count() / nx : 1;
+  ny = ny < 1 ? 1 : (ny > most ? most : ny);
   page_tables_kernel<<<dim3(nx, ny), kSeqs, 0, stream>>>(p);
   return cudaGetLastError();
 }
