@@ -6,21 +6,22 @@
 // over the 576-d latent rows c of every position up to the token's own (MQA
 // mode: all heads of a token attend the same rows).
 //
-// Both products are computed transposed.  A work item is up to N = 16, 32 or 64
-// query rows (heads of one token, or of a few tokens of one sequence) and a
-// range of 64-key tiles; per tile
+// This kernel: items of up to N = 16 or 32 query rows, one CTA each (a rank's heads
+// in decode); dense_mla_pair_sm100.cu has the one for more rows, dense_mla.cuh what
+// both share.  Both products are computed transposed.  An item is a few query rows
+// (heads of one token, or of a few tokens of one sequence) and a range of 64-key
+// tiles; per tile
 //     S^T [64 keys x N]  = C [64 x 576] . Q^T        (M = 64,  K = 576)
 //     O^T [512 x N]     += C[:, 0:512]^T . P^T        (4 x M = 128, K = 64)
 // so that the cache tile, as it lands by TMA, is the M-side operand of both
-// (K-major, then MN-major) and the few query rows are the N side.  With the rows
-// on the M side a 16-head rank would pay for 128 rows of tensor work, and 128
-// rows x 512 fp32 output dims would fill tensor memory and leave no room for the
-// scores; transposed, an item of 64 rows keeps 256 columns of O^T and two score
-// buffers in one CTA.
+// (K-major, then MN-major) and the few query rows are the N side: with the rows on
+// the M side a 16-head rank would pay for 128 rows of tensor work, and their 512
+// output dims would fill tensor memory.
 //
-// A CTA reads 72 KB per tile.  At the measured copy bandwidth an SM gets that
-// in ~3100 cycles; the tensor work of a tile is ~1900 (N = 64) and less for
-// fewer rows, so decode is bound by the cache read.
+// A CTA reads 72 KB per tile.  At the measured copy bandwidth (6.46 TB/s) an SM
+// gets that in ~3100 cycles; the tensor work of a tile is ~1600 (36 x 27 and 16 x 39
+// cycles measured, N = 16), so decode is bound by the cache read: 64 sequences of
+// 1K-32K positions at 16 heads 236 us, 5.4 TB/s, 83 % of the copy rate.
 //
 // Work split: the (sequence, row tiles) items of a launch are laid end to end
 // by their tile counts (plus a constant for an item's prologue and epilogue), and
@@ -705,7 +706,10 @@ cudaError_t launch(const DenseMlaParams& p, const DenseMaps& maps, int ctas, cud
 DensePlan dense_plan(const dsa_batch_t* b, int n_heads, bool shared) {
   DensePlan d;
   // Rows an item can hold: the rows of one sequence, or with a shared prefix
-  // of the whole batch.
+  // of the whole batch.  More than 32 go to CTA pairs: 64 sequences x 40 heads at 8K 147
+  // us against 221 in items of 32, 64 x 4 tokens x 16 heads 152 against 255 (items of 32
+  // are up to 2 us faster only where one to eight short sequences do not fill the GPU: 8 x
+  // 64 heads at 1000 keys 18.8 against 20.8).
   const int64_t rows = static_cast<int64_t>(shared ? b->total_q : b->max_q_per_seq) * n_heads;
   d.n = rows <= 16 ? 16 : (rows <= 32 ? 32 : 128);
   // Units that share a key range: the row tiles of an average sequence, in equal

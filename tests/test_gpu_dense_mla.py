@@ -25,6 +25,9 @@ CASES = [
     ([33, 2], [400, 129], 128, 64),                           # many row tiles, gangs
     ([1], [20000], 128, 64),                                  # one row split over many CTAs
     ([2, 1], [9000, 5], 16, 0),
+    # more sequences than a block has threads: the lengths are scanned in chunks
+    ([1] * 500, [1 + (37 * i) % 150 for i in range(500)], 4, 64),
+    ([(i % 3) for i in range(450)], [2 + (91 * i) % 130 for i in range(450)], 33, 0),
 ]
 
 
@@ -110,6 +113,7 @@ PREFIX = [
     (0, [1, 1], [20, 30], 16, 64),
     (3000, [1] * 33, [1 + 7 * i for i in range(33)], 16, 64),
     (129, [1, 0, 4], [1, 10, 4], 30, 64),
+    (200, [1] * 420, [1 + (13 * i) % 90 for i in range(420)], 4, 64),
 ]
 
 
@@ -166,3 +170,32 @@ def test_captured_and_replayed_with_new_lengths():
         g.replay()
         dsa.check_device_error(ws)
         check(out.cpu(), lse.cpu(), c.exact_dense(), c.rows)
+
+
+def test_same_bits_again_and_without_lse():
+    for c, prefix in ((Case([1, 3], [3000, 700], 16, 64, seed=12), None), (Case([2], [5000], 128, 0, seed=13), None),
+                      (Case([1, 2, 1], [700, 650, 900], 20, 64, seed=14, prefix=640), 640)):
+        first, z = c.dense(prefix)
+        again, _ = c.dense(prefix)
+        assert torch.equal(first.view(torch.int16), again.view(torch.int16))
+        out, _ = c.outputs(512)
+        op = dsa.OP_DENSE_MLA if prefix is None else dsa.OP_PREFIX_MLA
+        ws = dsa.workspace(op, c.batch, n_heads=c.heads)
+        if prefix is None:
+            dsa.dense_mla(c.batch, c.q.cuda(), c.cache.cuda(), c.scale, out, None, ws)
+        else:
+            dsa.prefix_mla(c.batch, prefix, c.q.cuda(), c.cache.cuda(), c.scale, out, None, ws)
+        dsa.check_device_error(ws)
+        assert torch.equal(first.view(torch.int16), out.cpu().view(torch.int16))
+
+
+def test_a_row_of_nan_queries_stays_alone():
+    c = Case([2, 1], [300, 90], 16, 64, seed=15)
+    want = c.exact_dense()
+    c.q[1, 5] = float("nan")
+    out, lse = c.dense()
+    assert torch.isnan(out[1, 5].float()).all() and torch.isnan(lse[1, 5])
+    keep = torch.ones((3, 16), dtype=torch.bool)
+    keep[1, 5] = False
+    d = (out.double() - want[0])[keep]
+    assert torch.isfinite(d).all() and d.norm() <= 2.0 ** -8 * want[0][keep].norm()

@@ -141,3 +141,54 @@ def test_more_tokens_than_the_host_said_is_a_bounds_error():
     assert e.value.status == 6
     assert (out[:256] == 0).all() and torch.isneginf(lse[:256]).all()
     assert (out[300:310].cpu().double() - want[0][300:]).norm() <= 2.0 ** -8 * want[0][300:].norm()
+
+
+def test_same_bits_again_and_without_lse():
+    for q, kv, heads in (([300, 5], [700, 40], 3), ([40], [4000], 2)):
+        c = Expanded(q, kv, heads, seed=8)
+        first, _ = c.run()
+        again, _ = c.run()
+        assert torch.equal(first.view(torch.int16), again.view(torch.int16))
+        out, _ = c.outputs(128)
+        ws = dsa.workspace(dsa.OP_EXPANDED_MLA, c.batch, n_heads=heads)
+        dsa.expanded_mla(c.batch, c.q.cuda(), c.up.cuda(), c.cache.cuda()[:, 512:], c.scale, out, None, ws)
+        dsa.check_device_error(ws)
+        assert torch.equal(first.view(torch.int16), out.cpu().view(torch.int16))
+
+
+def test_nan_and_infinite_scores_stay_in_their_rows():
+    c = Expanded([200], [500], 2, seed=9)
+    want = c.exact_expanded()
+    c.q[7, 1] = float("nan")
+    c.q[150, 0, 3] = float("inf")                   # scores of +-inf: NaN by the definition
+    out, lse = c.run()
+    for r, h in ((7, 1), (150, 0)):
+        assert torch.isnan(out[r, h].float()).all() and torch.isnan(lse[r, h])
+    keep = torch.ones((200, 2), dtype=torch.bool)
+    keep[7, 1] = keep[150, 0] = False
+    d = (out.double() - want[0])[keep]
+    assert torch.isfinite(d).all() and d.norm() <= 2.0 ** -8 * want[0][keep].norm()
+
+
+def test_captured_and_replayed_with_new_lengths():
+    c = Expanded([100, 60], [400, 200], 2, seed=10)
+    q, up, cache = c.q.cuda(), c.up.cuda(), c.cache.cuda()
+    out, lse = c.outputs(128)
+    ws = dsa.workspace(dsa.OP_EXPANDED_MLA, c.batch, n_heads=2)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        dsa.expanded_mla(c.batch, q, up, cache[:, 512:], c.scale, out, lse, ws)
+    torch.cuda.current_stream().wait_stream(s)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        dsa.expanded_mla(c.batch, q, up, cache[:, 512:], c.scale, out, lse, ws)
+    whole = c.at
+    for kv in ([400, 200], [130, 60], [257, 199]):
+        c.kv.copy_(torch.tensor(kv, dtype=torch.int32))
+        c.kv_len = kv
+        c.at = [a[:k] for a, k in zip(whole, kv)]
+        out.fill_(7.0)
+        g.replay()
+        dsa.check_device_error(ws)
+        check(out.cpu(), lse.cpu(), c.exact_expanded(), c.rows)
