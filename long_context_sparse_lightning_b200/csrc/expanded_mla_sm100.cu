@@ -59,7 +59,10 @@ struct Aux {
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];      // by tile parity
   uint64_t s_full[2], p_full[2], o_done[2];
   uint64_t drain;
-  uint64_t go, clean;       // the values before the border have landed / a border tile's are clean
+  uint64_t go;              // the values before the border have landed
+  // A border tile's values are clean, by turns: the two cleaning warps may be a tile
+  // apart, and both arrivals of a phase have to be for the same tile.
+  uint64_t clean[2];
   uint32_t tmem;
   int32_t any_bad;
   int32_t bad_pos[128];     // first position whose value of this dim is not finite, per dim
@@ -211,7 +214,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(&ax->drain, 1);
     mbar_init(&ax->go, 1);
-    mbar_init(&ax->clean, 2);
+    mbar_init(&ax->clean[0], 2);
+    mbar_init(&ax->clean[1], 2);
     fence_mbar_init();
     prefetch_tmap(&map_q);
     prefetch_tmap(&map_kv);
@@ -348,7 +352,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; ok && i < n_tiles; ++i) {
           wait(&ax->v_full[i & 1], (i >> 1) & 1, 624);
           if (i + 1 == border0) mbar_arrive(&ax->go);
-          if (i >= border0) wait(&ax->clean, (i - border0) & 1, 623);
+          if (i >= border0) wait(&ax->clean[(i - border0) & 1], ((i - border0) >> 1) & 1, 623);
 #pragma unroll
           for (int a = 0; a < 2; ++a) {
             const bool last = a == 1 || !two;
@@ -422,7 +426,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&ax->clean);
+        if (lane == 0) mbar_arrive(&ax->clean[(i - border0) & 1]);
       }
     }
   } else {
