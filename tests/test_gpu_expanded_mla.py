@@ -49,6 +49,10 @@ CASES = [
     ([100, 300, 1, 513], [100, 333, 513, 640], 4),
     ([64], [2000], 16),
     ([30], [30], 128),
+    # long prompts: CTA pairs, 512 rows an item; short sequences among them
+    ([1024], [1024], 19),
+    ([1100, 5, 257, 600], [1300, 5, 400, 601], 16),
+    ([1025, 0, 1], [1700, 9, 128], 25),
     # few rows, long contexts: the keys are split
     ([1], [5000], 2),
     ([200], [3001], 3),
@@ -65,28 +69,32 @@ def test_expanded_against_64_bits(q, kv, heads):
 
 
 def test_growing_scores():
-    for sign in (1.0, -1.0):
-        c = Expanded([300], [900], 2, seed=2)
-        c.up[c.at[0], :, 5] = (sign * torch.arange(900).float() / 900 * 600).to(torch.bfloat16)[:, None]
+    for sign, n, kv, heads in ((1.0, 300, 900, 2), (-1.0, 300, 900, 2), (1.0, 1030, 1100, 25), (-1.0, 1030, 1100, 25)):
+        c = Expanded([n], [kv], heads, seed=2)
+        c.up[c.at[0], :, 5] = (sign * torch.arange(kv).float() / kv * 600).to(torch.bfloat16)[:, None]
         c.q[:, :, 5] = 8.0
         out, lse = c.run()
         check(out, lse, c.exact_expanded(), c.rows)
 
 
-def test_values_at_positions_later_tokens_alone_see():
-    c = Expanded([300], [300], 1, seed=3)
+@pytest.mark.parametrize("n,heads,at,dim", [(300, 1, 200, 9), (1030, 25, 200, 9), (1030, 25, 700, 73), (1030, 25, 1026, 127)])
+def test_values_at_positions_later_tokens_alone_see(n, heads, at, dim):
+    c = Expanded([n], [n], heads, seed=3)
     want = c.exact_expanded()
-    row = c.at[0][200]
-    c.up[row, 0, 128 + 9] = float("nan")          # a value of position 200, dim 9
-    c.up[row + 50, 0, 3] = float("inf")           # a key of position 250
+    row = c.at[0][at]
+    c.up[row, 0, 128 + dim] = float("nan")        # a value of position `at`
+    if at + 50 < n:
+        c.up[row + 50, 0, 3] = float("inf")       # a key of a later one
     out, _ = c.run()
-    got = out[:300, 0].float()
-    assert torch.isfinite(got[:200]).all()
-    assert torch.isnan(got[200:, 9]).all()
-    assert torch.isfinite(got[200:250][:, [d for d in range(128) if d != 9]]).all()
-    d = (got[:200].double() - want[0][:200, 0]).abs()
-    A, e = want[2][:200, 0], want[3][:200, 0]
-    assert (d <= A * (2.0 ** -8 + 2 * e[:, None] + 2.0 ** -18) + 2.0 ** -8 * want[0][:200, 0].abs()).all()
+    got = out[:n, 0].float()
+    assert torch.isfinite(got[:at]).all()
+    assert torch.isnan(got[at:, dim]).all()
+    assert torch.isfinite(got[at:at + 50][:, [d for d in range(128) if d != dim]]).all()
+    d = (got[:at].double() - want[0][:at, 0]).abs()
+    A, e = want[2][:at, 0], want[3][:at, 0]
+    assert (d <= A * (2.0 ** -8 + 2 * e[:, None] + 2.0 ** -18) + 2.0 ** -8 * want[0][:at, 0].abs()).all()
+    for h in range(1, heads):                     # the other heads' values are theirs
+        assert (out[:n, h].double() - want[0][:, h]).norm() <= 2.0 ** -8 * want[0][:, h].norm()
 
 
 def test_bad_descriptors_are_bounds_errors():
@@ -144,7 +152,7 @@ def test_more_tokens_than_the_host_said_is_a_bounds_error():
 
 
 def test_same_bits_again_and_without_lse():
-    for q, kv, heads in (([300, 5], [700, 40], 3), ([40], [4000], 2)):
+    for q, kv, heads in (([300, 5], [700, 40], 3), ([1100], [1200], 30), ([40], [4000], 2)):
         c = Expanded(q, kv, heads, seed=8)
         first, _ = c.run()
         again, _ = c.run()
