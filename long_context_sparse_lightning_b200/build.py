@@ -19,9 +19,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libdsa.so")
 SOURCES = ["api.cu", "api_no_alloc.cu", "indexer_sm100.cu", "topk.cu", "sparse_mla_sm100.cu", "prep.cu",
-           "api_dense.cu", "dense_mla_sm100.cu", "dense_mla_pair_sm100.cu", "expanded_mla_sm100.cu",
-           "expanded_mla_pair_sm100.cu", "page_tables.cu"]
-HEADERS = ["ptx.cuh", "kernels.cuh", "select.cuh", "dense_mla.cuh", "expanded_mla.cuh"]
+           "api_dense.cu", "dense_mla_sm100.cu", "dense_mla_pair_sm100.cu", "expanded_mla_sm100.cu", "page_tables.cu"]
+HEADERS = ["ptx.cuh", "kernels.cuh", "select.cuh", "dense_mla.cuh"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 

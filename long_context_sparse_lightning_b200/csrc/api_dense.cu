@@ -166,16 +166,14 @@ dsa_status_t dsa_expanded_mla(const dsa_batch_t* b, const void* q, int32_t n_hea
   p.err = static_cast<uint32_t*>(ws);
   p.budget = dsa::wait_budget();
   const uint64_t h = static_cast<uint64_t>(n_heads);
-  const bool pairs = dsa::expanded_pairs(b, n_heads);
-  const uint64_t keys = static_cast<uint64_t>(b->total_keys);
-  dsa::ExpandedMaps maps;
-  if (!dsa::make_tmap_blocks(&maps.q, q, static_cast<uint64_t>(b->total_q), h * 3, h * 192, 128, 3) ||
-      !dsa::make_tmap_blocks(&maps.k, kv_up, keys, h * 4, h * 256, pairs ? 64 : 128, pairs ? 2 : 1) ||
-      !dsa::make_tmap_blocks(&maps.v, kv_up, keys, h * 4, h * 256, 128, 1) ||
-      !dsa::make_tmap_blocks(&maps.r, rope, keys, 1, static_cast<uint64_t>(rope_stride), pairs ? 64 : 128, 1))
+  CUtensorMap map_q, map_kv, map_r;
+  if (!dsa::make_tmap_blocks(&map_q, q, static_cast<uint64_t>(b->total_q), h * 3, h * 192, 128, 3) ||
+      !dsa::make_tmap_blocks(&map_kv, kv_up, static_cast<uint64_t>(b->total_keys), h * 4, h * 256, 128, 1) ||
+      !dsa::make_tmap_blocks(&map_r, rope, static_cast<uint64_t>(b->total_keys), 1, static_cast<uint64_t>(rope_stride),
+                             128, 1))
     return DSA_ERR_CUDA;
-  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  return (pairs ? dsa::launch_expanded_pair(p, maps, st) : dsa::launch_expanded_mla(p, maps, st)) == cudaSuccess
+  return dsa::launch_expanded_mla(p, map_q, map_kv, map_r, reinterpret_cast<cudaStream_t>(stream)) ==
+                 cudaSuccess
              ? DSA_OK
              : DSA_ERR_CUDA;
 }

@@ -31,7 +31,7 @@
 // the border the cleaning warps zero the value rows that no row of the CTA
 // sees, and for a non-finite value at a position that only later rows see they
 // zero it and note the first such position per dim: rows that do see it get NaN.
-#include "expanded_mla.cuh"
+#include "dense_mla.cuh"
 
 namespace dsa {
 namespace {
@@ -42,7 +42,6 @@ constexpr int kBlk = 128 * 128;            // one [128 rows x 64 dims] block, 12
 constexpr int kSlots = 8;                  // ring of key / value blocks, 3 + 2 per tile
 __device__ __forceinline__ int ring(int block) { return block & (kSlots - 1); }
 constexpr int64_t kL2Bytes = 64 << 20;     // of L2 that a group of heads may take
-constexpr int kPairRows = 1024;             // query tokens of a sequence from which on CTA pairs are faster
 constexpr int kSplitTiles = 3;             // key tiles a part of a split has at least
 constexpr int kThreads = 12 * 32;
 constexpr uint32_t kRegLow = 120, kRegHigh = 192;    // 128 * (120 + 2 * 192) = 384 * 168
@@ -70,7 +69,60 @@ struct Aux {
 };
 static_assert(sizeof(Aux) <= 1024, "");
 
-using namespace expanded;
+using dense::exp2_approx;
+using dense::finite_or_zero;
+using dense::kGrow;
+using dense::kLn2;
+using dense::pack_bf16;
+using dense::store_32;
+
+// f32x2 register pairs (low element first)
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 split(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
+// 2^x of two values on the FMA pipe: x = n + f with n an integer and |f| <= 1/2
+// (adding 1.5 * 2^23 rounds to n and leaves it in the low bits), 2^f by a degree-4
+// polynomial fitted for the smallest relative error on that range (2.7e-6 in fp32, far
+// below the rounding to bf16), n added to the exponent.  -125 <= x: what is smaller
+// gives 2^-125, so masked scores do not come here.
+__device__ __forceinline__ float2 exp2_poly(uint64_t x2) {
+  const float2 xv = split(x2);
+  const uint64_t x = pair(max_nan(xv.x, -125.f), max_nan(xv.y, -125.f));
+  const uint64_t big = pair(12582912.f, 12582912.f), minus = pair(-12582912.f, -12582912.f);
+  const uint64_t y = add2(x, big);
+  const uint64_t n = add2(y, minus);
+  const uint64_t f = fma2(n, pair(-1.f, -1.f), x);
+  uint64_t q = fma2(f, pair(0.009570101276040077f, 0.009570101276040077f), pair(0.05591786280274391f, 0.05591786280274391f));
+  q = fma2(q, f, pair(0.240247443318367f, 0.240247443318367f));
+  q = fma2(q, f, pair(0.6931217908859253f, 0.6931217908859253f));
+  q = fma2(q, f, pair(0.9999992847442627f, 0.9999992847442627f));
+  const float2 qv = split(q), yv = split(y);
+  return make_float2(__int_as_float(__float_as_int(qv.x) + (__float_as_int(yv.x) << 23)),
+                     __int_as_float(__float_as_int(qv.y) + (__float_as_int(yv.y) << 23)));
+}
 
 // What a CTA works on.
 struct Tile {
@@ -83,7 +135,8 @@ struct Tile {
 
 template <bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
-    expanded_mla_kernel(const ExpandedMlaParams p, const __grid_constant__ ExpandedMaps maps) {
+    expanded_mla_kernel(const ExpandedMlaParams p, const __grid_constant__ CUtensorMap map_q,
+                        const __grid_constant__ CUtensorMap map_kv, const __grid_constant__ CUtensorMap map_r) {
   // Block order: groups of heads whose keys and values fit L2 together, in a group the
   // longest rows of every head and sequence first (a head's longest row tiles, started
   // last, would run alone at the end: 8K at 16 heads, one head after the other, took 1.2 x).
@@ -164,10 +217,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&ax->clean[0], 2);
     mbar_init(&ax->clean[1], 2);
     fence_mbar_init();
-    prefetch_tmap(&maps.q);
-    prefetch_tmap(&maps.k);
-    prefetch_tmap(&maps.r);
-    prefetch_tmap(&maps.v);
+    prefetch_tmap(&map_q);
+    prefetch_tmap(&map_kv);
+    prefetch_tmap(&map_r);
   }
   if (tid < 128) ax->bad_pos[tid] = 0x7fffffff;
   if (tid == 0) ax->any_bad = 0;
@@ -200,9 +252,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint64_t* bar = &ax->k_full[i & 1];
           const int y = w.first_row_key + i * kKeys;
           mbar_arrive_expect_tx(bar, 3 * kBlk);
-          tma_load_3d(sm + OFF_KV + ring(5 * i) * kBlk, &maps.k, bar, 0, y, h * 4);
-          tma_load_3d(sm + OFF_KV + ring(5 * i + 1) * kBlk, &maps.k, bar, 0, y, h * 4 + 1);
-          tma_load_3d(sm + OFF_KV + ring(5 * i + 2) * kBlk, &maps.r, bar, 0, y, 0);
+          tma_load_3d(sm + OFF_KV + ring(5 * i) * kBlk, &map_kv, bar, 0, y, h * 4);
+          tma_load_3d(sm + OFF_KV + ring(5 * i + 1) * kBlk, &map_kv, bar, 0, y, h * 4 + 1);
+          tma_load_3d(sm + OFF_KV + ring(5 * i + 2) * kBlk, &map_r, bar, 0, y, 0);
           ++n_k;
         };
         auto values = [&](int i) {
@@ -211,13 +263,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint64_t* bar = &ax->v_full[i & 1];
           const int y = w.first_row_key + i * kKeys;
           mbar_arrive_expect_tx(bar, 2 * kBlk);
-          tma_load_3d(sm + OFF_KV + ring(5 * i + 3) * kBlk, &maps.v, bar, 0, y, h * 4 + 2);
-          tma_load_3d(sm + OFF_KV + ring(5 * i + 4) * kBlk, &maps.v, bar, 0, y, h * 4 + 3);
+          tma_load_3d(sm + OFF_KV + ring(5 * i + 3) * kBlk, &map_kv, bar, 0, y, h * 4 + 2);
+          tma_load_3d(sm + OFF_KV + ring(5 * i + 4) * kBlk, &map_kv, bar, 0, y, h * 4 + 3);
           ++n_v;
         };
         for (int a = 0; a < (two ? 2 : 1); ++a) {
           mbar_arrive_expect_tx(&ax->q_full[a], 3 * kBlk);
-          tma_load_3d(sm + OFF_Q + 3 * a * kBlk, &maps.q, &ax->q_full[a], 0, w.row0 + a * kRows, h * 3);
+          tma_load_3d(sm + OFF_Q + 3 * a * kBlk, &map_q, &ax->q_full[a], 0, w.row0 + a * kRows, h * 3);
           if (a == 0) keys(0);
         }
         values(0);
@@ -403,9 +455,83 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; ok && i < nt; ++i) {
       if (!wait(&ax->s_full[a], i & 1, 641)) break;
       tc_fence_after();
-      if (!softmax_tile(tS, tO, scale, lim - i * kKeys, warp_lim - i * kKeys < kKeys - 1, i == 0, m, l,
-                        [&] { return wait(&ax->o_done[a], (i - 1) & 1, 642); }))
-        break;
+      uint32_t s[4][32];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, s[c]);
+      tmem_ld_wait();
+      const int left = lim - i * kKeys;          // columns 0 .. left are seen
+      if (warp_lim - i * kKeys < kKeys - 1) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            if (32 * c + j > left) s[c][j] = __float_as_uint(NEG_INF);
+      }
+      // The row's maximum, NaN if any score is: such a row is NaN from here on.
+      float mx[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        mx[c] = __uint_as_float(s[c][0]);
+#pragma unroll
+        for (int j = 1; j < 32; ++j) mx[c] = max_nan(mx[c], __uint_as_float(s[c][j]));
+      }
+      const float top = max_nan(max_nan(mx[0], mx[1]), max_nan(mx[2], mx[3])) * scale;
+      const bool grow = !(top <= m + kGrow);     // true on the first tile that shows the row a key
+      if (__any_sync(0xffffffffu, grow)) {
+        const float f = grow ? exp2_approx(m - top) : 1.f;
+        if (grow) m = top < __int_as_float(0x7f800000) ? top : __int_as_float(0x7fffffff);      // an infinite score: NaN too
+        l *= f;
+        if (i > 0) {
+          if (!wait(&ax->o_done[a], (i - 1) & 1, 642)) break;
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < 8; ++c) {
+            uint32_t o[16];
+            asm volatile(
+                "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+                "%14, %15}, [%16];"
+                : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3]), "=r"(o[4]), "=r"(o[5]), "=r"(o[6]), "=r"(o[7]),
+                  "=r"(o[8]), "=r"(o[9]), "=r"(o[10]), "=r"(o[11]), "=r"(o[12]), "=r"(o[13]), "=r"(o[14]), "=r"(o[15])
+                : "r"(tO + 16 * c));
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+            tmem_st16(tO + 16 * c, o);
+          }
+        }
+      }
+      const float ref = m == NEG_INF ? 0.f : -m;
+      const uint64_t scale2 = pair(scale, scale), ref2 = pair(ref, ref);
+      uint64_t sum2 = pair(0.f, 0.f);
+      const bool masked = warp_lim - i * kKeys < kKeys - 1;
+      // Some of the exponentials go to the FMA pipe: the two row tiles' 32K at 16 a
+      // cycle would alone take 2048 cycles of a period.
+      auto probabilities = [&](int c, bool poly) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const uint64_t x = fma2(pair(__uint_as_float(s[c][2 * j]), __uint_as_float(s[c][2 * j + 1])), scale2, ref2);
+          float2 e;
+          if (poly && (j & 3) == 3) {
+            e = exp2_poly(x);
+          } else {
+            const float2 v = split(x);
+            e = make_float2(exp2_approx(v.x), exp2_approx(v.y));
+          }
+          sum2 = add2(sum2, pair(e.x, e.y));
+          pk[j] = pack_bf16(e.x, e.y);
+        }
+        tmem_st16(tS + 16 * c, pk);
+      };
+      if (masked) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) probabilities(c, false);
+      } else {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) probabilities(c, true);
+      }
+      const float2 sums = split(sum2);
+      l += sums.x + sums.y;
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
@@ -513,11 +639,8 @@ int expanded_splits(const dsa_batch_t* b, int n_heads) {
   return static_cast<int>(s < tiles / kSplitTiles ? s : (tiles / kSplitTiles > 1 ? tiles / kSplitTiles : 1));
 }
 
-bool expanded_pairs(const dsa_batch_t* b, int n_heads) {
-  return b->max_q_per_seq >= kPairRows && expanded_splits(b, n_heads) == 1;
-}
-
-cudaError_t launch_expanded_mla(const ExpandedMlaParams& p, const ExpandedMaps& maps, cudaStream_t stream) {
+cudaError_t launch_expanded_mla(const ExpandedMlaParams& p, const CUtensorMap& map_q, const CUtensorMap& map_kv,
+                                const CUtensorMap& map_r, cudaStream_t stream) {
   const auto kernel = p.splits > 1 ? expanded_mla_kernel<true> : expanded_mla_kernel<false>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
@@ -527,7 +650,7 @@ cudaError_t launch_expanded_mla(const ExpandedMlaParams& p, const ExpandedMaps& 
   q.head_group = static_cast<int>(fit < 1 ? 1 : (fit < p.n_heads ? fit : p.n_heads));
   const int64_t blocks = static_cast<int64_t>(q.row_tiles) * p.n_heads * p.num_seqs * p.splits;
   if (blocks >= (int64_t(1) << 31)) return cudaErrorInvalidConfiguration;
-  kernel<<<static_cast<unsigned>(blocks), kThreads, kSmem, stream>>>(q, maps);
+  kernel<<<static_cast<unsigned>(blocks), kThreads, kSmem, stream>>>(q, map_q, map_kv, map_r);
   const cudaError_t f = cudaGetLastError();
   if (f != cudaSuccess || p.splits == 1) return f;
   const int64_t rows = static_cast<int64_t>(p.total_q) * p.n_heads;

@@ -279,16 +279,10 @@ struct ExpandedMlaParams {
 };
 // Parts for a batch: 1 unless its row tiles leave half of the SMs idle.
 int expanded_splits(const dsa_batch_t* b, int n_heads);
-// Whether the batch goes to CTA pairs (512 rows an item) instead of single CTAs (256).
-bool expanded_pairs(const dsa_batch_t* b, int n_heads);
 // Descriptors (see make_tmap_blocks) of q as [total_q, H * 192], boxes of 3 x 128;
-// kv_up as [total_keys, H * 256] for keys and values and the RoPE dims [total_keys, 64]:
-//   single  k, r, v 1 x 128       pairs  k 2 x 64, r 1 x 64, v 1 x 128
-struct ExpandedMaps {
-  CUtensorMap q, k, r, v;
-};
-cudaError_t launch_expanded_mla(const ExpandedMlaParams& p, const ExpandedMaps& maps, cudaStream_t stream);
-cudaError_t launch_expanded_pair(const ExpandedMlaParams& p, const ExpandedMaps& maps, cudaStream_t stream);
+// kv_up as [total_keys, H * 256] and the RoPE dims [total_keys, 64], boxes of 1 x 128.
+cudaError_t launch_expanded_mla(const ExpandedMlaParams& p, const CUtensorMap& map_q, const CUtensorMap& map_kv,
+                                const CUtensorMap& map_r, cudaStream_t stream);
 
 // ------------------------------------------------------------ page tables --
 struct PageTablesParams {

@@ -49,7 +49,7 @@ CASES = [
     ([100, 300, 1, 513], [100, 333, 513, 640], 4),
     ([64], [2000], 16),
     ([30], [30], 128),
-    # long prompts: CTA pairs, 512 rows an item; short sequences among them
+    # long prompts, short sequences among them
     ([1024], [1024], 19),
     ([1100, 5, 257, 600], [1300, 5, 400, 601], 16),
     ([1025, 0, 1], [1700, 9, 128], 25),
