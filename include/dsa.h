@@ -26,6 +26,12 @@
  *   dsa_quantize_fp8,   upstream of the three: the per-128 FP8 quantiser of q / k
  *   dsa_cache_write     and the write of new tokens into the key and latent caches.
  *
+ * Beside them, for layers and contexts without a selection:
+ *   dsa_dense_mla       the third stage over every position s <= t (absorbed form);
+ *   dsa_prefix_mla      the same for sequences that share their first positions;
+ *   dsa_expanded_mla    the same attention in the expanded (MHA) form, for prompts;
+ *   dsa_page_tables     a paged step's arrays from its requests' lengths.
+ *
  * Conventions (all entry points):
  *   - Every tensor pointer is caller-owned DEVICE memory, row-major and
  *     contiguous, 16-byte aligned.  The library never allocates, never frees
@@ -129,7 +135,12 @@ typedef struct {
  * (dsa_forward: only where it takes the fused kernel, see dsa_indexer_topk).
  * For DSA_OP_TOPK (and the unfused forward) rows longer than 32768 positions
  * with k_sel a multiple of 4 add 8 * k_sel bytes per row and 32768-position
- * segment: the candidates of the two-phase selection. */
+ * segment: the candidates of the two-phase selection.  The dense attentions
+ * (which do not read k_sel) hold their partial results there: up to 39 MB for
+ * DSA_OP_DENSE_MLA and 16 bytes a row, plus 4 KB a row (query token and
+ * head) for DSA_OP_PREFIX_MLA; for DSA_OP_EXPANDED_MLA 516 bytes a row and key
+ * split where the rows of the batch's bounds alone would leave SMs idle, else
+ * 256 bytes (so a smaller batch may need more than a larger one). */
 DSA_API size_t dsa_workspace_size(dsa_op_t op, const dsa_batch_t* batch, int32_t k_sel, int32_t n_heads);
 
 /* Indexer scores.
@@ -278,8 +289,8 @@ DSA_API dsa_status_t dsa_sparse_mla_no_alloc(const dsa_batch_t* batch, const voi
  *   q    [total_q, n_heads, 576] bf16     kv [total_keys, 576] bf16 latent cache
  *   out  [total_q, n_heads, 512] bf16     lse [total_q, n_heads] fp32 or NULL
  *   1 <= n_heads <= 128; ws of dsa_workspace_size(DSA_OP_DENSE_MLA, batch, 0,
- *   n_heads) bytes (k_sel is not read).  Two launches; sequences of any mix of
- *   lengths and of 0 or more query tokens each.
+ *   n_heads) bytes (k_sel is not read).  Two launches (none with total_q = 0);
+ *   sequences of any mix of lengths and of 0 or more query tokens each.
  * Arithmetic: bf16 products accumulated in fp32 on the tensor cores, softmax
  * in fp32, probabilities rounded to bf16 for the second product (relative
  * 2^-8 each at most), one rounding to bf16 at the end.

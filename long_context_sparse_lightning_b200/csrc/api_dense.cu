@@ -57,7 +57,8 @@ dsa_status_t run_dense(const dsa_batch_t* b, int prefix_len, const void* q, int 
   const bool shared = prefix_len >= 0;
   const dsa_status_t s = dsa::validate_batch(b);
   if (s != DSA_OK) return s;
-  if (q == nullptr || kv == nullptr || out == nullptr) return DSA_ERR_INVALID_ARG;
+  // a step without tokens may come with empty tensors
+  if (b->total_q > 0 && (q == nullptr || kv == nullptr || out == nullptr)) return DSA_ERR_INVALID_ARG;
   if (misaligned(q, 16) || misaligned(kv, 16) || misaligned(out, 16) || misaligned(lse, 4)) return DSA_ERR_INVALID_ARG;
   if (!(sm_scale > 0.f) || !std::isfinite(sm_scale)) return DSA_ERR_INVALID_ARG;
   if (n_heads < 1 || n_heads > 128) return DSA_ERR_UNSUPPORTED;
@@ -137,7 +138,7 @@ dsa_status_t dsa_expanded_mla(const dsa_batch_t* b, const void* q, int32_t n_hea
                               dsa_stream_t stream) {
   const dsa_status_t s = dsa::validate_batch(b);
   if (s != DSA_OK) return s;
-  if (q == nullptr || kv_up == nullptr || rope == nullptr || out == nullptr) return DSA_ERR_INVALID_ARG;
+  if (b->total_q > 0 && (q == nullptr || kv_up == nullptr || rope == nullptr || out == nullptr)) return DSA_ERR_INVALID_ARG;
   if (misaligned(q, 16) || misaligned(kv_up, 16) || misaligned(rope, 16) || misaligned(out, 16) || misaligned(lse, 4))
     return DSA_ERR_INVALID_ARG;
   if (rope_stride < 64 || rope_stride % 8 != 0 || rope_stride >= (int64_t(1) << 31)) return DSA_ERR_INVALID_ARG;

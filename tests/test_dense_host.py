@@ -75,7 +75,8 @@ def test_dense_refusals():
     assert dense(c, n=need - 1) == WORKSPACE
     assert dense(host_batch(B=0)) == INVALID and dense(host_batch(max_q=11)) == INVALID
     assert dense(host_batch(page=96)) == INVALID and dense(host_batch(page=64, blocks=1)) == INVALID
-    assert dense(host_batch(total_q=0, max_q=0)) == 0             # nothing to do
+    # nothing to do, also with empty tensors
+    assert dense(host_batch(total_q=0, max_q=0)) == 0 and dense(host_batch(total_q=0, max_q=0), q=None, out=None) == 0
 
 
 def test_prefix_refusals():
@@ -98,7 +99,8 @@ def test_expanded_refusals():
     assert expanded(c, n=255) == WORKSPACE
     long = host_batch(B=1, total_q=10, max_q=10, max_kv=8192, total_keys=8192)
     assert expanded(long, n=256) == WORKSPACE                     # the split's partial results
-    assert expanded(host_batch(total_q=0, max_q=0)) == 0
+    none = host_batch(total_q=0, max_q=0)
+    assert expanded(none) == 0 and expanded(none, q=None, up=None, rope=None, out=None) == 0
 
 
 def tables(n=2, q=0x100000, before=0x200000, free=0x300000, n_free=4, page=64, table=0x400000, blocks=3, tokens=8,

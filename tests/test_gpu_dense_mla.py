@@ -199,3 +199,20 @@ def test_a_row_of_nan_queries_stays_alone():
     keep[1, 5] = False
     d = (out.double() - want[0])[keep]
     assert torch.isfinite(d).all() and d.norm() <= 2.0 ** -8 * want[0][keep].norm()
+
+
+def test_a_step_without_tokens():
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    bf = lambda *s: torch.empty(s, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    paged = dsa.Batch(i32(0, 0), i32(70), None, 0, 0, 70, 128, block_table=i32(1, 0).view(1, 2), page_size=64)
+    flat = dsa.Batch(i32(0, 0), i32(70), torch.zeros(1, dtype=torch.int64, device="cuda"), 0, 0, 70, 128)
+    lse = torch.empty((0, 16), device="cuda")
+    for op, call in ((dsa.OP_DENSE_MLA, lambda ws: dsa.dense_mla(paged, bf(0, 16, 576), bf(128, 576), 1.0, bf(0, 16, 512),
+                                                                 lse, ws)),
+                     (dsa.OP_PREFIX_MLA, lambda ws: dsa.prefix_mla(paged, 64, bf(0, 16, 576), bf(128, 576), 1.0,
+                                                                   bf(0, 16, 512), lse, ws)),
+                     (dsa.OP_EXPANDED_MLA, lambda ws: dsa.expanded_mla(flat, bf(0, 16, 192), bf(128, 16, 256), bf(128, 64),
+                                                                       1.0, bf(0, 16, 128), lse, ws))):
+        ws = dsa.workspace(op, flat if op == dsa.OP_EXPANDED_MLA else paged, 0, 16)
+        call(ws)
+        dsa.check_device_error(ws)
