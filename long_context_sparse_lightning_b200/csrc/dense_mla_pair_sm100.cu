@@ -28,8 +28,8 @@
 // covered by the next tile's S anyway).
 //
 // Tensor memory of one CTA (M = 128 over a pair: lanes 0-63 hold the rows'
-// first N / 2 columns, lanes 64-127 the others): O at [0, 256), two score
-// buffers of 32 columns.
+// first N / 2 columns, lanes 64-127 the others): O at [0, 256), three score
+// buffers of 32 columns behind it (S runs two tiles ahead of O).
 //
 // Roles per CTA: warp 0 items and TMA of the keys, warp 1 MMAs (rank 0), warp 2
 // TMA of the second half, warps 4-7 and 8-11 softmax of every other tile and epilogue
