@@ -269,7 +269,9 @@ struct ExpandedMlaParams {
   uint16_t* out = nullptr;            // bf16 [total_q, H, 128]
   float* lse = nullptr;               // [total_q, H] or nullptr
   int32_t max_q = 0;                  // most query tokens of a sequence (the grid's)
-  int32_t row_tiles = 0;              // set by the launch: blocks of rows per sequence and head,
+  int32_t row_tiles = 0;              // set by the launch: row tiles of max_q tokens,
+  int32_t blocks = 0;                 // row tiles per head in the grid,
+  int32_t listed = 0;                 // which are looked up from cu_q, not one per row tile and sequence,
   int32_t head_group = 0;             // heads that run side by side
   int32_t splits = 1;                 // parts the key tiles of a row tile are split into
   float* part_lse = nullptr;          // splits > 1: [splits, total_q, H] log2 units

@@ -151,6 +151,34 @@ def test_more_tokens_than_the_host_said_is_a_bounds_error():
     assert (out[300:310].cpu().double() - want[0][300:]).norm() <= 2.0 ** -8 * want[0][300:].norm()
 
 
+@pytest.mark.parametrize("q,kv,heads", [
+    ([700] + [3] * 20, [900] + [5 + i for i in range(20)], 2),                   # most blocks look up their row tile
+    ([3] * 400 + [600, 0, 257] + [1] * 30, [4] * 400 + [600, 3, 300] + [9] * 30, 1),     # more sequences than threads
+    ([600, 2, 0, 5, 1, 1], [6000, 4000, 7, 900, 3000, 1], 1),                    # and the keys are split
+])
+def test_one_long_sequence_among_short_ones(q, kv, heads):
+    c = Expanded(q, kv, heads, seed=12)
+    out, lse = c.run()
+    check(out, lse, c.exact_expanded(), c.rows)
+
+
+def test_rows_of_too_many_tokens_are_zero():
+    # the grid's last row tile of the sequence takes the rows behind it, whichever way the blocks find their tiles
+    for q, kv, max_q in (([600, 10], [600, 40], 256), ([900] + [4] * 12, [900] + [30] * 12, 600), ([300], [5000], 200)):
+        c = Expanded(q, kv, 1, seed=13)
+        want = c.exact_expanded()
+        c.batch.c.max_q_per_seq = max_q
+        out, lse = c.outputs(128)
+        ws = dsa.workspace(dsa.OP_EXPANDED_MLA, c.batch, n_heads=1)
+        dsa.expanded_mla(c.batch, c.q.cuda(), c.up.cuda(), c.cache.cuda()[:, 512:], c.scale, out, lse, ws)
+        with pytest.raises(dsa.DSAError) as e:
+            dsa.check_device_error(ws)
+        assert e.value.status == 6
+        n = q[0]
+        assert (out[:n] == 0).all() and torch.isneginf(lse[:n]).all()
+        assert (out[n:c.rows].cpu().double() - want[0][n:]).norm() <= 2.0 ** -8 * want[0][n:].norm()
+
+
 def test_same_bits_again_and_without_lse():
     for q, kv, heads in (([300, 5], [700, 40], 3), ([1100], [1200], 30), ([40], [4000], 2)):
         c = Expanded(q, kv, heads, seed=8)
