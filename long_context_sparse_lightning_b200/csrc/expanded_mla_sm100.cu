@@ -4,7 +4,8 @@
 // the caller's up-projection) and the 64 RoPE dims kr that all heads share:
 // 640 multiply-adds per head and pair against the absorbed form's 1088.
 //
-// A CTA owns two tiles of 128 query rows of one head (lane = row) and walks
+// A CTA owns two tiles of 128 query rows of one head (lane = row; or, of a
+// sequence's few rows, one tile of two heads, whose key tiles then alternate) and walks
 // the keys up to its last row's position in tiles of 128.  Tensor memory: the two
 // tiles' scores (128 columns each) and outputs (128 each), all 512 columns; a tile's
 // probabilities overwrite its scores as bf16 and are the A operand of the
@@ -51,7 +52,7 @@ constexpr uint32_t TM_S = 0, TM_O = 256;   // + 128 * tile
 constexpr int OFF_Q = 0;                               // 2 tiles x 3 blocks
 constexpr int OFF_KV = 6 * kBlk;
 constexpr int OFF_AUX = OFF_KV + kSlots * kBlk;
-constexpr int kSmem = OFF_AUX + 1024 + 1024;
+constexpr int kSmem = OFF_AUX + 1536 + 1024;
 static_assert(kSmem <= 232448, "shared memory of one CTA");
 
 struct Aux {
@@ -65,9 +66,9 @@ struct Aux {
   uint64_t clean[2];
   uint32_t tmem;
   int32_t any_bad;
-  int32_t bad_pos[128];     // first position whose value of this dim is not finite, per dim
+  int32_t bad_pos[2][128];  // first position whose value of this dim is not finite, per head of the CTA and dim
 };
-static_assert(sizeof(Aux) <= 1024, "");
+static_assert(sizeof(Aux) <= 1536, "");
 
 using dense::exp2_approx;
 using dense::finite_or_zero;
@@ -131,6 +132,7 @@ struct Tile {
   int n[2];                // key tiles of the two row tiles (0: nothing to do)
   int first_row_key;       // cache row of the first key
   bool bad;
+  bool duo;                // the row tiles are the same rows of heads h and h + 1
 };
 
 // Row tile `j` of the batch's, the highest of their sequences first (equal ones in the
@@ -211,12 +213,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   // Block order: groups of heads whose keys and values fit L2 together, in a group the
   // longest rows of every head and sequence first (a head's longest row tiles, started
   // last, would run alone at the end: 8K at 16 heads, one head after the other, took 1.2 x).
-  const int per_group = p.blocks * p.splits * p.head_group;
+  const int per_group = p.blocks * p.splits * p.head_group, units = (p.n_heads + p.head_step - 1) / p.head_step;
   const int group = static_cast<int>(blockIdx.x) / per_group;
-  const int heads = min(p.head_group, p.n_heads - group * p.head_group);
+  const int heads = min(p.head_group, units - group * p.head_group);
   const int in_group = static_cast<int>(blockIdx.x) - group * per_group;
   const int in_heads = in_group / heads;
-  const int h = group * p.head_group + in_group - in_heads * heads;
+  const int h = (group * p.head_group + in_group - in_heads * heads) * p.head_step;
   const int j = SPLIT ? in_heads / p.splits : in_heads, part = SPLIT ? in_heads - j * p.splits : 0;
   int b, qt;
   if (p.listed) {
@@ -260,22 +262,33 @@ __global__ void __launch_bounds__(kThreads, 1)
     w.base -= t0 * kKeys;
     w.first_row_key += t0 * kKeys;
   }
+  w.duo = !SPLIT && p.duo && !w.bad && w.rows <= kRows && (h | 1) < p.n_heads;
+  if (w.duo) {
+    if (h & 1) return;                       // with the head before
+    w.n[1] = w.n[0];
+  }
   if (w.bad || max(w.n[0], w.n[1]) == 0) {
     if (w.bad && qt == 0 && h == 0 && part == 0 && tid == 0) report_error(p.err, kDevErrBounds, 602, b);
     if (!SPLIT) {
-      for (int u = tid; u < w.rows * 16; u += kThreads)
-        *reinterpret_cast<uint4*>(p.out + (static_cast<int64_t>(w.row0 + (u >> 4)) * H + h) * 128 + (u & 15) * 8) =
-            make_uint4(0, 0, 0, 0);
+      for (int g = h; g < min(h + p.head_step, H); ++g)
+        for (int u = tid; u < w.rows * 16; u += kThreads)
+          *reinterpret_cast<uint4*>(p.out + (static_cast<int64_t>(w.row0 + (u >> 4)) * H + g) * 128 + (u & 15) * 8) =
+              make_uint4(0, 0, 0, 0);
     }
     float* lse = SPLIT ? p.part_lse + part_rows * H : p.lse;
     if (lse != nullptr)
-      for (int r = tid; r < w.rows; r += kThreads)
-        lse[static_cast<int64_t>(w.row0 + r) * H + h] = __int_as_float(0xff800000);
+      for (int g = h; g < min(h + p.head_step, H); ++g)
+        for (int r = tid; r < w.rows; r += kThreads)
+          lse[static_cast<int64_t>(w.row0 + r) * H + g] = __int_as_float(0xff800000);
     return;
   }
-  const int n_tiles = max(w.n[0], w.n[1]);
+  // Key tiles pass the ring one after the other; of two heads in turn (tile g of the
+  // ring is key tile g / 2 of head h + (g & 1)).
+  const int duo = w.duo ? 1 : 0;
+  const int n_tiles = max(w.n[0], w.n[1]) << duo;
   const bool two = w.n[1] > 0;
-  const int border0 = w.base < 0 ? 0 : (w.base + 1) / kKeys;      // first tile with a position that row 0 must not see
+  // first tile with a position that row 0 must not see
+  const int border0 = w.base < 0 ? 0 : ((w.base + 1) / kKeys) << duo;
 
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -304,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefetch_tmap(&map_kv);
     prefetch_tmap(&map_r);
   }
-  if (tid < 128) ax->bad_pos[tid] = 0x7fffffff;
+  if (tid < 256) ax->bad_pos[tid >> 7][tid & 127] = 0x7fffffff;
   if (tid == 0) ax->any_bad = 0;
   if (warp == 1) {
     tmem_alloc(&ax->tmem, kTmemCols);
@@ -333,10 +346,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           // blocks 5 i .. 5 i + 2 of the ring take the place of the last of K(i - 2) and of V(i - 2)
           if (i >= 2 && !wait(&ax->v_empty[i & 1], ((i >> 1) + 1) & 1)) return;
           uint64_t* bar = &ax->k_full[i & 1];
-          const int y = w.first_row_key + i * kKeys;
+          const int y = w.first_row_key + (i >> duo) * kKeys, hh = h + (i & duo);
           mbar_arrive_expect_tx(bar, 3 * kBlk);
-          tma_load_3d(sm + OFF_KV + ring(5 * i) * kBlk, &map_kv, bar, 0, y, h * 4);
-          tma_load_3d(sm + OFF_KV + ring(5 * i + 1) * kBlk, &map_kv, bar, 0, y, h * 4 + 1);
+          tma_load_3d(sm + OFF_KV + ring(5 * i) * kBlk, &map_kv, bar, 0, y, hh * 4);
+          tma_load_3d(sm + OFF_KV + ring(5 * i + 1) * kBlk, &map_kv, bar, 0, y, hh * 4 + 1);
           tma_load_3d(sm + OFF_KV + ring(5 * i + 2) * kBlk, &map_r, bar, 0, y, 0);
           ++n_k;
         };
@@ -344,15 +357,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           // blocks 5 i + 3 and 5 i + 4 that of the first two of K(i - 1)
           if (i >= 1 && !wait(&ax->k_empty[(i - 1) & 1], ((i - 1) >> 1) & 1)) return;
           uint64_t* bar = &ax->v_full[i & 1];
-          const int y = w.first_row_key + i * kKeys;
+          const int y = w.first_row_key + (i >> duo) * kKeys, hh = h + (i & duo);
           mbar_arrive_expect_tx(bar, 2 * kBlk);
-          tma_load_3d(sm + OFF_KV + ring(5 * i + 3) * kBlk, &map_kv, bar, 0, y, h * 4 + 2);
-          tma_load_3d(sm + OFF_KV + ring(5 * i + 4) * kBlk, &map_kv, bar, 0, y, h * 4 + 3);
+          tma_load_3d(sm + OFF_KV + ring(5 * i + 3) * kBlk, &map_kv, bar, 0, y, hh * 4 + 2);
+          tma_load_3d(sm + OFF_KV + ring(5 * i + 4) * kBlk, &map_kv, bar, 0, y, hh * 4 + 3);
           ++n_v;
         };
         for (int a = 0; a < (two ? 2 : 1); ++a) {
           mbar_arrive_expect_tx(&ax->q_full[a], 3 * kBlk);
-          tma_load_3d(sm + OFF_Q + 3 * a * kBlk, &map_q, &ax->q_full[a], 0, w.row0 + a * kRows, h * 3);
+          tma_load_3d(sm + OFF_Q + 3 * a * kBlk, &map_q, &ax->q_full[a], 0, w.row0 + (w.duo ? 0 : a * kRows),
+                      (w.duo ? h + a : h) * 3);
           if (a == 0) keys(0);
         }
         values(0);
@@ -413,13 +427,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (n1 > n0) {
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk)
-              umma_f16_ts(d_o, d_s + kk * 8, vd + ((kk * 2048) >> 4), idesc_o, (i | kk) ? 1u : 0u);
+              umma_f16_ts(d_o, d_s + kk * 8, vd + ((kk * 2048) >> 4), idesc_o, ((i >> duo) | kk) ? 1u : 0u);
           } else {
             const uint64_t vd1 = v_desc + n1 * (kBlk >> 4);
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk) {
-              umma_f16_ts(d_o, d_s + kk * 8, vd + ((kk * 2048) >> 4), idesc_half, (i | kk) ? 1u : 0u);
-              umma_f16_ts(d_o + 64, d_s + kk * 8, vd1 + ((kk * 2048) >> 4), idesc_half, (i | kk) ? 1u : 0u);
+              umma_f16_ts(d_o, d_s + kk * 8, vd + ((kk * 2048) >> 4), idesc_half, ((i >> duo) | kk) ? 1u : 0u);
+              umma_f16_ts(d_o + 64, d_s + kk * 8, vd1 + ((kk * 2048) >> 4), idesc_half, ((i >> duo) | kk) ? 1u : 0u);
             }
           }
           umma_commit(&ax->o_done[a]);
@@ -430,12 +444,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         wait(&ax->k_full[0], 0, 621);
         if (two) wait(&ax->q_full[1], 0, 620);
         tc_fence_after();
-        if (ok && w.n[0] > 0) scores(0, 0, !two);
-        if (ok && two) scores(1, 0, true);
+        if (ok && w.n[0] > 0) scores(0, 0, w.duo || !two);
+        if (ok && two && (!w.duo || wait(&ax->k_full[1], 0, 625))) {
+          tc_fence_after();
+          scores(1, duo, true);
+        }
         for (int i = 0; ok && i < n_tiles; ++i) {
           wait(&ax->v_full[i & 1], (i >> 1) & 1, 624);
           if (i + 1 == border0) mbar_arrive(&ax->go);
           if (i >= border0) wait(&ax->clean[(i - border0) & 1], ((i - border0) >> 1) & 1, 623);
+          if (w.duo) {
+            // One head's product each; the next keys land over tiles that are done, so the next
+            // scores of both heads follow the second's product.
+            if (!wait(&ax->p_full[i & 1], (i >> 1) & 1, 622)) break;
+            tc_fence_after();
+            values(i & 1, i, true);
+            for (int g = i + 1; ok && (i & 1) != 0 && g < min(i + 3, n_tiles); ++g)
+              if (wait(&ax->k_full[g & 1], (g >> 1) & 1, 625)) {
+                tc_fence_after();
+                scores(g & 1, g, true);
+              }
+            continue;
+          }
 #pragma unroll
           for (int a = 0; a < 2; ++a) {
             const bool last = a == 1 || !two;
@@ -470,8 +500,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = border0; ok && i < n_tiles; ++i) {
         wait(&ax->v_full[i & 1], (i >> 1) & 1);
         if (!ok) break;
-        const int first = max(0, w.base + 1 - i * kKeys);               // the rows before are seen by every row
-        const int dead = min(kKeys, w.base + w.rows - i * kKeys);       // rows from here on by none
+        const int key0 = (i >> duo) * kKeys;
+        const int first = max(0, w.base + 1 - key0);               // the rows before are seen by every row
+        const int dead = min(kKeys, w.base + w.rows - key0);       // rows from here on by none
 #pragma unroll 1
         for (int c = 0; c < 2; ++c) {
           uint4* blk = reinterpret_cast<uint4*>(sm + OFF_KV + ring(5 * i + 3 + c) * kBlk);
@@ -500,7 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int e = 0; e < 8; ++e) {
                 const uint32_t mask = 0x7F80u << (16 * (e & 1));
                 if ((x[e >> 1] & mask) == mask) {
-                  atomicMin(&ax->bad_pos[c * 64 + 8 * ((u & 7) ^ (r & 7)) + e], i * kKeys + r);
+                  atomicMin(&ax->bad_pos[i & duo][c * 64 + 8 * ((u & 7) ^ (r & 7)) + e], key0 + r);
                   ax->any_bad = 1;
                 }
               }
@@ -517,13 +548,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ----------------------------------------------------- softmax, epilogue --
     const int a = static_cast<int>(warp >> 2) - 1;
     const uint32_t quarter = warp & 3u;
-    const int r = a * kRows + static_cast<int>(quarter * 32 + lane);     // row of the CTA
+    const int r0 = w.duo ? 0 : a * kRows, r = r0 + static_cast<int>(quarter * 32 + lane);     // row of the CTA
     const uint32_t t_lane = tmem + ((quarter * 32u) << 16);
     const uint32_t tS = t_lane + TM_S + 128 * a, tO = t_lane + TM_O + 128 * a;
     const float scale = p.scale_log2, NEG_INF = __int_as_float(0xff800000);
     // rows behind the last one follow it (their results are not stored)
     const int lim = w.base + min(r, w.rows - 1);
-    const int warp_lim = w.base + min(a * kRows + static_cast<int>(quarter * 32), w.rows - 1);
+    const int warp_lim = w.base + min(r0 + static_cast<int>(quarter * 32), w.rows - 1);
     bool ok = true;
     auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t site) {
       if (ok && !mbar_wait(bar, parity, p.budget)) {
@@ -623,7 +654,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (ok && nt > 0 && wait(&ax->o_done[a], (nt - 1) & 1, 643)) {
       tc_fence_after();
       const float inv = l == 0.f ? 0.f : 1.f / l;      // 0: a part of the keys that the row does not see
-      const int64_t at = static_cast<int64_t>(w.row0 + r) * H + h;
+      const int64_t at = static_cast<int64_t>(w.row0 + r) * H + h + (w.duo ? a : 0);
 #pragma unroll 1
       for (int c = 0; c < 4; c += 2) {
         uint32_t o[2][32];
@@ -633,7 +664,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ax->any_bad != 0) {
 #pragma unroll
           for (int j = 0; j < 64; ++j)
-            if (ax->bad_pos[32 * c + j] <= lim) o[j >> 5][j & 31] = 0x7FFFFFFFu;
+            if (ax->bad_pos[w.duo ? a : 0][32 * c + j] <= lim) o[j >> 5][j & 31] = 0x7FFFFFFFu;
         }
         if (SPLIT && r < w.rows) {
           float* to = p.part_o + (part_rows * H + at) * 128 + 32 * c;
@@ -739,8 +770,17 @@ cudaError_t launch_expanded_mla(const ExpandedMlaParams& p, const CUtensorMap& m
   q.blocks = static_cast<int>(q.listed ? most : every);
   const int64_t seen = static_cast<int64_t>(p.num_seqs) * p.max_kv_len;
   const int64_t fit = kL2Bytes / ((p.total_keys < seen ? p.total_keys : seen) * 512);      // heads' keys and values in L2
-  q.head_group = static_cast<int>(fit < 1 ? 1 : (fit < p.n_heads ? fit : p.n_heads));
-  const int64_t blocks = (q.listed ? most : every) * p.n_heads * p.splits;
+  // Two heads per block where a row tile holds at most 128 rows: a block of few rows is a chain of
+  // latencies (~7 us for one key tile), and two chains take little longer (16 x 100 tokens at
+  // 128 heads 126 -> 92 us, 500 x 40 at 16 391 -> 237, 2 x 5 tokens at 128 heads, 256 blocks, 38 -> 31).
+  // Not where the GPU has an SM for every block or nearly so (6 ragged prompts at 16 heads, 128 blocks
+  // of 192 in use: 25.6 -> 27.8).
+  q.duo = p.splits == 1 && p.n_heads > 1 && 2 * (q.listed ? most : every) * p.n_heads > 3 * sm_count() ? 1 : 0;
+  q.head_step = q.duo && p.max_q <= kRows ? 2 : 1;
+  const int units = (p.n_heads + q.head_step - 1) / q.head_step;
+  const int64_t group = fit / q.head_step;
+  q.head_group = static_cast<int>(group < 1 ? 1 : (group < units ? group : units));
+  const int64_t blocks = (q.listed ? most : every) * units * p.splits;
   if (blocks >= (int64_t(1) << 31)) return cudaErrorInvalidConfiguration;
   kernel<<<static_cast<unsigned>(blocks), kThreads, kSmem, stream>>>(q, map_q, map_kv, map_r);
   const cudaError_t f = cudaGetLastError();

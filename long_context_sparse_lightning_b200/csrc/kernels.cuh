@@ -272,7 +272,9 @@ struct ExpandedMlaParams {
   int32_t row_tiles = 0;              // set by the launch: row tiles of max_q tokens,
   int32_t blocks = 0;                 // row tiles per head in the grid,
   int32_t listed = 0;                 // which are looked up from cu_q, not one per row tile and sequence,
-  int32_t head_group = 0;             // heads that run side by side
+  int32_t duo = 0;                    // row tiles of at most 128 rows are walked for two heads by one block,
+  int32_t head_step = 1;              // 2: all of them are (a block per two heads),
+  int32_t head_group = 0;             // heads (pairs of them) that run side by side
   int32_t splits = 1;                 // parts the key tiles of a row tile are split into
   float* part_lse = nullptr;          // splits > 1: [splits, total_q, H] log2 units
   float* part_o = nullptr;            // splits > 1: [splits, total_q, H, 128] normalised

@@ -162,6 +162,31 @@ def test_one_long_sequence_among_short_ones(q, kv, heads):
     check(out, lse, c.exact_expanded(), c.rows)
 
 
+@pytest.mark.parametrize("q,kv,heads", [
+    ([100] * 4, [100, 129, 700, 257], 128),                   # two heads a block, 1 to 6 key tiles of each
+    ([3, 128, 1, 0, 128, 60], [300, 128, 1, 9, 500, 60], 127),   # the last head alone
+    ([257, 40, 128, 129], [300, 40, 640, 1000], 128),         # blocks of one and of two heads
+    ([300] + [5] * 40, [300] + [140 + i for i in range(40)], 33),
+])
+def test_two_heads_per_block(q, kv, heads):
+    c = Expanded(q, kv, heads, seed=14)
+    out, lse = c.run()
+    check(out, lse, c.exact_expanded(), c.rows)
+
+
+def test_values_that_are_not_finite_stay_with_their_head_and_rows():
+    # of two heads in a block, at a position that later rows alone see
+    c = Expanded([90, 70, 5], [220, 70, 5], 128, seed=15)
+    want = c.exact_expanded()
+    at, head = 60, 41
+    c.up[c.at[0][130 + at], head, 128 + 7] = float("inf")
+    out, lse = c.run()
+    bad = torch.isnan(out.float())
+    assert bad[at:90, head, 7].all() and int(bad.sum()) == 90 - at
+    d = (out.double() - want[0])[~bad]
+    assert d.norm() <= 2.0 ** -8 * want[0][~bad].norm()
+
+
 def test_rows_of_too_many_tokens_are_zero():
     # the grid's last row tile of the sequence takes the rows behind it, whichever way the blocks find their tiles
     for q, kv, max_q in (([600, 10], [600, 40], 256), ([900] + [4] * 12, [900] + [30] * 12, 600), ([300], [5000], 200)):
