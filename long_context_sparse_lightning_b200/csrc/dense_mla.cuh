@@ -50,7 +50,7 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 }
 
 // 32 bytes to a 16-byte aligned address.
-__device__ __forceinline__ void store_32(void* dst, const uint32_t (&v)[8]) {
+__device__ __forceinline__ void store_32(void* dst, const uint32_t* v) {
   if ((reinterpret_cast<uintptr_t>(dst) & 31u) == 0) {
     st_global_32(dst, v);
   } else {

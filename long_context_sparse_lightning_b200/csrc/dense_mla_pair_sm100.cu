@@ -86,6 +86,54 @@ struct Aux {
 };
 static_assert(sizeof(Aux) <= 2048, "");
 
+// Four neighbouring lanes hold four pieces of 8 words each: piece q of lane j goes to
+// lane q as its piece j.
+__device__ __forceinline__ void exchange_4(uint32_t (&v)[32], uint32_t lane) {
+#pragma unroll
+  for (int bit = 1; bit <= 2; bit <<= 1) {
+    const bool up = (lane & bit) != 0;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      if (q & bit) continue;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        uint32_t &lo = v[8 * q + e], &hi = v[8 * (q | bit) + e];
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? lo : hi, bit);
+        if (up) {
+          lo = got;
+        } else {
+          hi = got;
+        }
+      }
+    }
+  }
+}
+
+// Keys that some row must not see: 0 x a non-finite value would reach that row, so
+// such values become 0 in the tile.  A row that does see the key has its NaN from
+// the score.  By the 128 threads of a warpgroup; not inlined: its code between a
+// tile's softmax and the next costs the tiles that have no border (16K samples prefix 253 us, so 245).
+__device__ __noinline__ void clean_values(uint8_t* stage, int pos0, int lo, int min_lim, int st) {
+#pragma unroll 1
+  for (int u0 = st; u0 < 8 * kBlk / 16; u0 += 8 * 128) {      // (four loads' latency at once)
+    uint4* w = reinterpret_cast<uint4*>(stage) + u0;
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      const int pos = pos0 + 32 * (u0 >> 10) + ((u0 >> 3) & 15) + 16 * g;
+      if (pos >= lo && pos <= min_lim) continue;
+      uint4 a[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) a[q] = w[256 * q + 128 * g];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const uint4 b = make_uint4(finite_or_zero(a[q].x), finite_or_zero(a[q].y), finite_or_zero(a[q].z),
+                                   finite_or_zero(a[q].w));
+        if (a[q].x != b.x || a[q].y != b.y || a[q].z != b.z || a[q].w != b.w) w[256 * q + 128 * g] = b;
+      }
+    }
+  }
+}
+
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     dense_pair_kernel(const DenseMlaParams p, const __grid_constant__ DenseMaps maps) {
   extern __shared__ uint8_t smem_raw[];
@@ -165,9 +213,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (r < 0 && rank == 0) report_error(p.err, kDevErrBounds, 504, walk.e.b);
         return r < 0 ? -1 : static_cast<int>(r);
       };
-      int my_row = tile_row(static_cast<int>(lane)), my_next = tile_row(32 + static_cast<int>(lane));
       publish(it);
       if (!ok || it.n_tiles == 0) continue;
+      int my_row = tile_row(static_cast<int>(lane)), my_next = tile_row(32 + static_cast<int>(lane));
       if (n_q > 0) wait(&ax->q_free, (n_q - 1) & 1, 551);
       if (!ok) break;
       ++n_q;
@@ -453,20 +501,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                        "r"(pk[4 * u]), "r"(pk[4 * u + 1]), "r"(pk[4 * u + 2]), "r"(pk[4 * u + 3])
                        : "memory");
         wait(&ax->v_full[s], (t / kStages) & 1, 584);
-        if (border) {
-          // Keys that some row must not see: 0 x a non-finite value would reach that
-          // row, so such values become 0 in the tile.  A row that does see the key
-          // has its NaN from the score.
-#pragma unroll 1
-          for (int u = st; u < 8 * kBlk / 16; u += 128) {
-            const int pos = pos0 + 32 * (u >> 10) + ((u >> 3) & 31);
-            if (pos >= it.lo && pos <= min_lim) continue;
-            uint4* w = reinterpret_cast<uint4*>(sm + OFF_KV + s * kStage) + u;
-            const uint4 a = *w;
-            const uint4 b = make_uint4(finite_or_zero(a.x), finite_or_zero(a.y), finite_or_zero(a.z), finite_or_zero(a.w));
-            if (a.x != b.x || a.y != b.y || a.z != b.z || a.w != b.w) *w = b;
-          }
-        }
+        if (border) clean_values(sm + OFF_KV + s * kStage, pos0, it.lo, min_lim, st);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive_remote(p_full0 + 8 * (t & 1));
@@ -492,37 +527,47 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tc_fence_after();
       }
       float* dst32 = fp32_rows(p, it, kN);
+      // 64 dims at a time.  A thread has a row's, which would go out as 32 rows' sectors an
+      // instruction; four lanes exchange theirs first, so that each row gets whole lines (16K
+      // samples prefix 249 -> 245 us; the piece of one short item still takes ~5700 cycles, 128
+      // KB out of one SM).
+      const int row4 = n & ~3;                 // the first of the four lanes' rows
+      const int piece = 8 * static_cast<int>(lane & 3u);
 #pragma unroll 1
-      for (int c = 128 * wg; c < 128 * wg + 128; c += 32) {
-        uint32_t o[32];
+      for (int c = 128 * wg; c < 128 * wg + 128; c += 64) {
+        uint32_t o[2][32];
         if (it.n_tiles > 0) {
-          tmem_ld32(t_lane + c, o);
+          tmem_ld32(t_lane + c, o[0]);
+          tmem_ld32(t_lane + c + 32, o[1]);
           tmem_ld_wait();
         } else {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) o[j] = 0u;
+          for (int j = 0; j < 64; ++j) o[j >> 5][j & 31] = 0u;
         }
         const int d = 256 * half + c;
-        if (n < it.rows && dst32 != nullptr && it.n_tiles > 0) {    // an empty piece has lse = -inf, its output is not read
-          float* at = dst32 + static_cast<int64_t>(n) * 512 + d;
+        if (dst32 != nullptr) {
+          if (it.n_tiles > 0) {                // an empty piece has lse = -inf, its output is not read
 #pragma unroll
-          for (int j = 0; j < 32; j += 8) {
-            uint32_t v[8];
+            for (int g = 0; g < 2; ++g) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = __float_as_uint(__uint_as_float(o[j + e]) * inv);
-            store_32(at + j, v);
+              for (int j = 0; j < 32; ++j) o[g][j] = __float_as_uint(__uint_as_float(o[g][j]) * inv);
+              exchange_4(o[g], lane);
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                if (row4 + q < it.rows)
+                  store_32(dst32 + static_cast<int64_t>(row4 + q) * 512 + d + 32 * g + piece, &o[g][8 * q]);
+            }
           }
-        }
-        if (n < it.rows && dst32 == nullptr) {
-          uint16_t* at = p.out + static_cast<int64_t>(it.row0 + n) * 512 + d;
+        } else {
+          uint32_t v[32];
 #pragma unroll
-          for (int j = 0; j < 32; j += 16) {
-            uint32_t v[8];
+          for (int j = 0; j < 32; ++j)
+            v[j] = pack_bf16(__uint_as_float(o[j >> 4][2 * (j & 15)]) * inv, __uint_as_float(o[j >> 4][2 * (j & 15) + 1]) * inv);
+          exchange_4(v, lane);
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              v[e] = pack_bf16(__uint_as_float(o[j + 2 * e]) * inv, __uint_as_float(o[j + 2 * e + 1]) * inv);
-            store_32(at + j, v);
-          }
+          for (int q = 0; q < 4; ++q)
+            if (row4 + q < it.rows)
+              store_32(p.out + static_cast<int64_t>(it.row0 + row4 + q) * 512 + d + 2 * piece, &v[8 * q]);
         }
         __syncwarp();
       }

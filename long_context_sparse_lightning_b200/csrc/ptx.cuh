@@ -276,7 +276,7 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* m, uin
 }
 
 // 32 bytes to a 32-byte aligned address: a whole sector per lane.
-__device__ __forceinline__ void st_global_32(void* dst, const uint32_t (&v)[8]) {
+__device__ __forceinline__ void st_global_32(void* dst, const uint32_t* v) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]),
                "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                : "memory");
