@@ -167,11 +167,27 @@ def test_one_long_sequence_among_short_ones(q, kv, heads):
     ([3, 128, 1, 0, 128, 60], [300, 128, 1, 9, 500, 60], 127),   # the last head alone
     ([257, 40, 128, 129], [300, 40, 640, 1000], 128),         # blocks of one and of two heads
     ([300] + [5] * 40, [300] + [140 + i for i in range(40)], 33),
+    ([700] + [3] * 20, [900] + [5 + i for i in range(20)], 17),  # and the blocks look up their row tile
 ])
 def test_two_heads_per_block(q, kv, heads):
     c = Expanded(q, kv, heads, seed=14)
     out, lse = c.run()
     check(out, lse, c.exact_expanded(), c.rows)
+
+
+def test_a_bad_descriptor_of_two_heads_per_block():
+    c = Expanded([40] * 4, [50, 60, 40, 300], 127, seed=16)
+    want = c.exact_expanded()
+    c.start[1] = c.total_keys - 5
+    out, lse = c.outputs(128)
+    ws = dsa.workspace(dsa.OP_EXPANDED_MLA, c.batch, n_heads=127)
+    dsa.expanded_mla(c.batch, c.q.cuda(), c.up.cuda(), c.cache.cuda()[:, 512:], c.scale, out, lse, ws)
+    with pytest.raises(dsa.DSAError) as e:
+        dsa.check_device_error(ws)
+    assert e.value.status == 6
+    assert (out[40:80] == 0).all() and torch.isneginf(lse[40:80]).all()
+    keep = [r for r in range(160) if not 40 <= r < 80]
+    assert (out.cpu().double() - want[0])[keep].norm() <= 2.0 ** -8 * want[0][keep].norm()
 
 
 def test_values_that_are_not_finite_stay_with_their_head_and_rows():
