@@ -119,6 +119,30 @@ __device__ __forceinline__ void ld_cols16(uint32_t t, uint32_t (&r)[16]) {
       : "r"(t));
 }
 
+// Keys that some row must not see: 0 x a non-finite value would reach that row, so
+// such values become 0 in the tile (its pairs are slots n, n + 1, n + 2, n + 3 of the ring).
+// A row that does see the key has its NaN from the score.  By 128 threads; not
+// inlined, to stay out of the tiles that have no border.
+template <int SLOTS>
+__device__ __noinline__ void clean_values(uint8_t* pairs, int n, int pos0, int lo, int min_lim, int st) {
+#pragma unroll 1
+  for (int g = 0; g < 4; ++g) {                // key st / 8 + 16 g, eight units of it
+    const int pos = pos0 + (st >> 3) + 16 * g;
+    if (pos >= lo && pos <= min_lim) continue;
+    uint4 a[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      a[q] = reinterpret_cast<const uint4*>(pairs + (n + (q >> 1)) % SLOTS * kPair + (q & 1) * kBlk)[st + 128 * g];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const uint4 b = make_uint4(finite_or_zero(a[q].x), finite_or_zero(a[q].y), finite_or_zero(a[q].z),
+                                 finite_or_zero(a[q].w));
+      if (a[q].x != b.x || a[q].y != b.y || a[q].z != b.z || a[q].w != b.w)
+        reinterpret_cast<uint4*>(pairs + (n + (q >> 1)) % SLOTS * kPair + (q & 1) * kBlk)[st + 128 * g] = b;
+    }
+  }
+}
+
 template <int N>
 __global__ void __launch_bounds__(kThreads, 1)
     dense_mla_kernel(const DenseMlaParams p, const __grid_constant__ DenseMaps maps) {
@@ -460,24 +484,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (border) {
-          // Keys that some row must not see: 0 x a non-finite value would reach that
-          // row, so such values become 0 in the tile.  A row that does see the key
-          // has its NaN from the score.
 #pragma unroll 1
-          for (int m = 0; m < 4; ++m) {
-            const int n = 4 * t + m, ps = n % C::PAIR_SLOTS;
-            wait(&ax->pair_full[ps], (n / C::PAIR_SLOTS) & 1, 534);
-            uint8_t* blk = sm + C::OFF_PAIR + ps * kPair;
-#pragma unroll 1
-            for (int u = st; u < kPair / 16; u += kSoftThreads) {
-              const int pos = pos0 + ((u >> 3) & 63);
-              if (pos >= it.lo && pos <= min_lim) continue;
-              uint4* w = reinterpret_cast<uint4*>(blk) + u;
-              const uint4 a = *w;
-              const uint4 b = make_uint4(finite_or_zero(a.x), finite_or_zero(a.y), finite_or_zero(a.z), finite_or_zero(a.w));
-              if (a.x != b.x || a.y != b.y || a.z != b.z || a.w != b.w) *w = b;
-            }
-          }
+          for (int m = 0; m < 4; ++m)
+            wait(&ax->pair_full[(4 * t + m) % C::PAIR_SLOTS], ((4 * t + m) / C::PAIR_SLOTS) & 1, 534);
+          clean_values<C::PAIR_SLOTS>(sm + C::OFF_PAIR, 4 * t, pos0, it.lo, min_lim, st);
         }
         fence_proxy_async_smem();
         __syncwarp();
