@@ -83,6 +83,17 @@ __device__ __forceinline__ uint32_t finite_or_zero(uint32_t w) {
   return w;
 }
 
+// True where one of the eight bf16 values is not finite (an exponent of all ones
+// carries into its half's top bit).
+__device__ __forceinline__ bool any_not_finite(const uint4& v) {
+  const uint32_t t = ((v.x & 0x7F807F80u) + 0x00800080u) | ((v.y & 0x7F807F80u) + 0x00800080u) |
+                     ((v.z & 0x7F807F80u) + 0x00800080u) | ((v.w & 0x7F807F80u) + 0x00800080u);
+  return (t & 0x80008000u) != 0;
+}
+__device__ __forceinline__ uint4 finite_or_zero(const uint4& v) {
+  return make_uint4(finite_or_zero(v.x), finite_or_zero(v.y), finite_or_zero(v.z), finite_or_zero(v.w));
+}
+
 // Entry v of the launch's work list.  With a shared prefix entry 0 is the prefix
 // (every row of the batch, positions 0 .. prefix-1) and entry v > 0 the rest
 // of sequence v - 1; without one entry v is sequence v.

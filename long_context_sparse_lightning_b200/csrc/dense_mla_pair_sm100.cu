@@ -125,11 +125,8 @@ __device__ __noinline__ void clean_values(uint8_t* stage, int pos0, int lo, int 
 #pragma unroll
       for (int q = 0; q < 4; ++q) a[q] = w[256 * q + 128 * g];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const uint4 b = make_uint4(finite_or_zero(a[q].x), finite_or_zero(a[q].y), finite_or_zero(a[q].z),
-                                   finite_or_zero(a[q].w));
-        if (a[q].x != b.x || a[q].y != b.y || a[q].z != b.z || a[q].w != b.w) w[256 * q + 128 * g] = b;
-      }
+      for (int q = 0; q < 4; ++q)
+        if (any_not_finite(a[q])) w[256 * q + 128 * g] = finite_or_zero(a[q]);
     }
   }
 }

@@ -134,12 +134,10 @@ __device__ __noinline__ void clean_values(uint8_t* pairs, int n, int pos0, int l
     for (int q = 0; q < 8; ++q)
       a[q] = reinterpret_cast<const uint4*>(pairs + (n + (q >> 1)) % SLOTS * kPair + (q & 1) * kBlk)[st + 128 * g];
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      const uint4 b = make_uint4(finite_or_zero(a[q].x), finite_or_zero(a[q].y), finite_or_zero(a[q].z),
-                                 finite_or_zero(a[q].w));
-      if (a[q].x != b.x || a[q].y != b.y || a[q].z != b.z || a[q].w != b.w)
-        reinterpret_cast<uint4*>(pairs + (n + (q >> 1)) % SLOTS * kPair + (q & 1) * kBlk)[st + 128 * g] = b;
-    }
+    for (int q = 0; q < 8; ++q)
+      if (any_not_finite(a[q]))
+        reinterpret_cast<uint4*>(pairs + (n + (q >> 1)) % SLOTS * kPair + (q & 1) * kBlk)[st + 128 * g] =
+            finite_or_zero(a[q]);
   }
 }
 

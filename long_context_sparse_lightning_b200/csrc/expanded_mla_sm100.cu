@@ -511,22 +511,19 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
           for (int u0 = 8 * first + tid - 64; u0 < 8 * dead; u0 += 4 * 64) {
             uint4 v[4];
-            uint32_t t = 0;
+            bool any = false;
 #pragma unroll
             for (int q = 0; q < 4; ++q) v[q] = u0 + 64 * q < 8 * dead ? blk[u0 + 64 * q] : make_uint4(0, 0, 0, 0);
-            // an exponent of all ones carries into its half's top bit
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-              t |= ((v[q].x & 0x7F807F80u) + 0x00800080u) | ((v[q].y & 0x7F807F80u) + 0x00800080u) |
-                   ((v[q].z & 0x7F807F80u) + 0x00800080u) | ((v[q].w & 0x7F807F80u) + 0x00800080u);
-            if ((t & 0x80008000u) == 0) continue;
+            for (int q = 0; q < 4; ++q) any |= dense::any_not_finite(v[q]);
+            if (!any) continue;
 #pragma unroll 1
             for (int q = 0; q < 4; ++q) {
               const int u = u0 + 64 * q, r = u >> 3;
               if (u >= 8 * dead) break;
               const uint4 a = blk[u];
               const uint32_t x[4] = {a.x, a.y, a.z, a.w};
-              blk[u] = make_uint4(finite_or_zero(a.x), finite_or_zero(a.y), finite_or_zero(a.z), finite_or_zero(a.w));
+              blk[u] = finite_or_zero(a);
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
                 const uint32_t mask = 0x7F80u << (16 * (e & 1));
