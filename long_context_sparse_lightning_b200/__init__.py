@@ -13,6 +13,7 @@ binding's entry points raises.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -247,13 +248,16 @@ class Batch:
         kv_before[b] positions and takes q_len[b] new tokens, whose pages come from free_pages in order and are
         entered in block_table.  The host sizes may be bounds, as for a captured step: total_q rows are the
         padded count.  Returns the batch, the rows' positions (indexer_prep's pos) and cache rows, and the
-        number of pages taken (int32 [1])."""
-        device = q_len.device
-        cu_q = torch.empty(q_len.numel() + 1, dtype=torch.int32, device=device)
-        kv_len = torch.empty(q_len.numel(), dtype=torch.int32, device=device)
-        pos = torch.empty(total_q, dtype=torch.int32, device=device)
-        slots = torch.empty(total_q, dtype=torch.int64, device=device)
-        used = torch.empty(1, dtype=torch.int32, device=device)
+        number of pages taken (int32 [1]).  These tensors are allocated on the stream that fills them (`stream`, or the
+        current one): another stream waits for it before it reads them, and calls record_stream on what it may still be
+        reading when the last reference goes."""
+        with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+            device = q_len.device
+            cu_q = torch.empty(q_len.numel() + 1, dtype=torch.int32, device=device)
+            kv_len = torch.empty(q_len.numel(), dtype=torch.int32, device=device)
+            pos = torch.empty(total_q, dtype=torch.int32, device=device)
+            slots = torch.empty(total_q, dtype=torch.int64, device=device)
+            used = torch.empty(1, dtype=torch.int32, device=device)
         page_tables(q_len, kv_before, free_pages, page_size, block_table, cu_q, kv_len, pos, slots, used, ws, stream)
         batch = Batch(cu_q, kv_len, None, total_q, max_q_per_seq, max_kv_len, total_keys, block_table=block_table,
                       page_size=page_size)

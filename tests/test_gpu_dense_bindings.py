@@ -1,0 +1,29 @@
+"""The bindings of the dense attentions and the page tables on a GPU: a batch made on another
+stream than the current one."""
+
+import pytest
+import torch
+
+import long_context_sparse_lightning_b200 as dsa
+
+pytestmark = pytest.mark.gpu
+
+
+def test_from_requests_on_another_stream_leaves_freed_memory_of_the_current_one():
+    # blocks that are free again on the current stream may still be read there by queued work
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    q_len, before, free = i32(2, 1), i32(0, 64), i32(5, 6, 7)
+    table, ws = torch.full((2, 3), -1, dtype=torch.int32, device="cuda"), torch.zeros(256, dtype=torch.uint8, device="cuda")
+    table[1, 0] = 1
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    olds = [torch.full((n,), 9, dtype=torch.int32, device="cuda") for n in (3, 2, 4, 8, 1) for _ in range(8)]
+    torch.cuda._sleep(100_000_000)                    # ~50 ms: the copies below wait behind it
+    copies = [x.clone() for x in olds]
+    del olds
+    batch, pos, slots, used = dsa.Batch.from_requests(q_len, before, free, 64, table, ws, 4, 2, 65, 512, side)
+    torch.cuda.synchronize()
+    assert all((c == 9).all() for c in copies)
+    assert batch.cu_q.tolist() == [0, 2, 3] and batch.kv_len.tolist() == [2, 65] and used.tolist() == [2]
+    assert pos.tolist() == [0, 1, 64, 0] and slots.tolist() == [320, 321, 384, -1]
+    dsa.check_device_error(ws, side)
