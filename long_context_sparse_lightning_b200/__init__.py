@@ -209,6 +209,12 @@ class Batch:
         if block_table is not None and (block_table.dtype != torch.int32 or block_table.dim() != 2
                                         or not block_table.is_contiguous()):
             raise TypeError("block_table must be a contiguous int32 [num_seqs, blocks_per_seq] tensor")
+        # kernels read these by address: all of num_seqs entries, on the device that the calls check cu_q to be on
+        for t, n in ((cu_q, kv_len.shape[0] + 1), (kv_len, 0), (kv_start, kv_len.shape[0]),
+                     (block_table, kv_len.shape[0] if block_table is not None else 0)):
+            if t is not None and (t.device != cu_q.device or not t.is_contiguous() or t.shape[0] < n):
+                raise ValueError("Batch: contiguous cu_q [num_seqs + 1], kv_len [num_seqs], kv_start [num_seqs] and "
+                                 "block_table [num_seqs, blocks_per_seq] on one device")
         self.cu_q, self.kv_len, self.kv_start, self.block_table = cu_q, kv_len, kv_start, block_table
         self.num_seqs = int(kv_len.shape[0])
         self.total_q = int(total_q)

@@ -3,6 +3,7 @@ device a call's memory and work belong to, and arrays that must not reach a kern
 
 import contextlib
 
+import pytest
 import torch
 
 import long_context_sparse_lightning_b200 as dsa
@@ -39,3 +40,18 @@ def test_from_requests_allocates_on_the_stream_that_writes(monkeypatch):
                                                           torch.zeros(256, dtype=torch.uint8), 4, 2, 6, 320, stream)
         assert seen == [stream] * 5 and launched[-1] == stream and not inside
         assert batch.total_q == 4 and pos.numel() == slots.numel() == 4 and used.numel() == 1
+
+
+def test_batch_arrays_lie_together():
+    # a host array, one on another device, a strided or a short one would be read at the wrong addresses
+    cu, kv, start, table = ints(0, 2, 3), ints(5, 9), torch.tensor([0, 5]), torch.zeros((2, 2), dtype=torch.int32)
+    make = lambda cu=cu, kv=kv, start=start, table=None: dsa.Batch(cu, kv, start, 3, 2, 9, 128, block_table=table,  # noqa: E731
+                                                                  page_size=64 if table is not None else 0)
+    make()
+    make(start=None, table=table)
+    make(cu=ints(0, 2, 3, 0, 0), start=torch.tensor([0, 5, 0]), table=torch.zeros((4, 2), dtype=torch.int32))  # spare entries
+    for bad in (dict(kv=kv.to("meta")), dict(start=start.to("meta")), dict(table=table.to("meta")), dict(cu=cu.to("meta")),
+                dict(cu=ints(0, 9, 2, 9, 3)[::2]), dict(kv=ints(5, 0, 9, 0)[::2]), dict(start=torch.tensor([0, 9, 5, 9])[::2]),
+                dict(cu=ints(0, 2)), dict(start=torch.tensor([0])), dict(table=table[:1])):
+        with pytest.raises(ValueError):
+            make(**bad)
