@@ -165,16 +165,19 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _launch(fn, where, device, stream, *args):
-    """fn(*args, stream) on device number `device`, on its current stream unless one is given."""
+def _call(fn, where, device, stream, *args):
+    """fn(*args, stream)'s status on device number `device`, on its current stream unless one is given."""
     if device < 0:
         raise ValueError(f"{where}: tensors on a CUDA device")
     handle = _raw_stream(device) if stream is None else stream.cuda_stream
     if device == torch.cuda.current_device():
-        status = fn(*args, handle)
-    else:
-        with torch.cuda.device(device):
-            status = fn(*args, handle)
+        return fn(*args, handle)
+    with torch.cuda.device(device):
+        return fn(*args, handle)
+
+
+def _launch(fn, where, device, stream, *args):
+    status = _call(fn, where, device, stream, *args)
     if status != 0:
         raise DSAError(status, where)
 
@@ -433,10 +436,12 @@ def cache_write(batch: Batch, k, latent, k_cache, k_scale, latent_cache, ws, str
 
 
 def check_device_error(ws, stream=None):
-    """Synchronise, read and clear the workspace's device error word; raise if set."""
+    """Synchronise (the current stream of the workspace's device, or `stream`), read and clear the workspace's device
+    error word; raise if set."""
     site = ctypes.c_uint32(0)
     info = ctypes.c_uint32(0)
-    st = _lib().dsa_check_device_error(_ptr(ws), _stream(stream), ctypes.byref(site), ctypes.byref(info))
+    st = _call(lambda p, handle: _lib().dsa_check_device_error(p, handle, ctypes.byref(site), ctypes.byref(info)),
+               "check_device_error", ws.get_device(), stream, _ptr(ws))
     if st != 0:
         err = DSAError(st, f"device error (site {site.value}, info {info.value})")
         err.site, err.info = site.value, info.value

@@ -55,3 +55,55 @@ def test_batch_arrays_lie_together():
                 dict(cu=ints(0, 2)), dict(start=torch.tensor([0])), dict(table=table[:1])):
         with pytest.raises(ValueError):
             make(**bad)
+
+
+def test_errors_are_read_behind_the_stream_of_the_workspaces_device(monkeypatch):
+    # a call whose tensors lie on another device than the current one runs on that device's stream: so
+    # does the wait before its error word is read
+    seen = []
+
+    class Guard:
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            seen.append(self.index)
+
+        def __exit__(self, *a):
+            seen.append(-1)
+
+    class Ws:
+        def __init__(self, index):
+            self.index = index
+
+        def get_device(self):
+            return self.index
+
+        def is_contiguous(self):
+            return True
+
+        def data_ptr(self):
+            return 4096
+
+    class Lib:
+        @staticmethod
+        def dsa_check_device_error(ws, stream, site, info):
+            seen.append((ws, stream))
+            return 0
+
+    class Stream:
+        cuda_stream = 77
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "device", Guard)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: Stream)
+    monkeypatch.setattr(dsa, "_raw_stream", lambda index: 1000 + index)
+    monkeypatch.setattr(dsa, "_lib", lambda: Lib)
+    dsa.check_device_error(Ws(1))
+    assert seen == [1, (4096, 1001), -1]
+    del seen[:]
+    dsa.check_device_error(Ws(0))
+    dsa.check_device_error(Ws(0), Stream)
+    assert seen == [(4096, 1000), (4096, 77)]
+    with pytest.raises(ValueError, match="CUDA"):
+        dsa.check_device_error(torch.zeros(256, dtype=torch.uint8))
