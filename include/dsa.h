@@ -334,8 +334,10 @@ DSA_API dsa_status_t dsa_prefix_mla(const dsa_batch_t* batch, int32_t prefix_len
  *   DSA_ERR_UNSUPPORTED: the expanded rows are made for the call).
  *   ws of DSA_OP_EXPANDED_MLA bytes.
  * Arithmetic, masked positions, rows behind the last sequence and bad descriptors (q_len >
- * max_q_per_seq among them) as dsa_dense_mla; a non-finite value that a row does
- * see makes that output NaN. */
+ * max_q_per_seq among them) as dsa_dense_mla.  Of what a row does see, a value that
+ * is not finite (infinities too) makes that output NaN, a NaN score or one of +inf the
+ * whole row; a key of score -inf has weight 0, and a row of only such keys gets out = 0,
+ * lse = -inf. */
 DSA_API dsa_status_t dsa_expanded_mla(const dsa_batch_t* batch, const void* q, int32_t n_heads, const void* kv_up,
                                       const void* rope, int64_t rope_stride, float sm_scale, void* out, float* lse,
                                       void* ws, size_t ws_bytes, dsa_stream_t stream);

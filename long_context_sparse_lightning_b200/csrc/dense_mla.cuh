@@ -22,6 +22,9 @@ constexpr int kItemCost = N == 128 ? 6 : 2;
 constexpr int kMinShare = 3;              // tiles (and item costs) a gang takes at least (1, 2, 3, 4: one request of 1000
                                           // keys at 16 heads 15.2, 15.2, 14.6, 15.9 us)
 constexpr float kLn2 = 0.69314718055994531f;
+// Log-sum-exp (log2 units) of a piece with keys none of which has a weight for the row: of
+// weight 0 like an empty piece's -inf, but written, and a NaN in it counts.
+constexpr float kNoWeight = -3e38f;
 
 struct Item {
   int32_t n_tiles;      // -1: no more items

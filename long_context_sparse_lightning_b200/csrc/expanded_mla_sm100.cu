@@ -31,7 +31,8 @@
 // and 0 x a non-finite value would reach that row all the same.  So in tiles on
 // the border the cleaning warps zero the value rows that no row of the CTA
 // sees, and for a non-finite value at a position that only later rows see they
-// zero it and note the first such position per dim: rows that do see it get NaN.
+// zero it and note the first such position per dim: rows that do see it get NaN,
+// as from every other tile (the epilogue turns infinite sums into NaN).
 #include "dense_mla.cuh"
 
 namespace dsa {
@@ -74,6 +75,7 @@ using dense::exp2_approx;
 using dense::finite_or_zero;
 using dense::kGrow;
 using dense::kLn2;
+using dense::kNoWeight;
 using dense::pack_bf16;
 using dense::store_32;
 
@@ -96,6 +98,11 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   uint64_t d;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
 __device__ __forceinline__ float max_nan(float a, float b) {
@@ -650,7 +657,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (ok && nt > 0 && wait(&ax->o_done[a], (nt - 1) & 1, 643)) {
       tc_fence_after();
-      const float inv = l == 0.f ? 0.f : 1.f / l;      // 0: a part of the keys that the row does not see
+      // 0: no key has a weight, those of a part that the row does not see or scores of -inf throughout
+      const float inv = l == 0.f || m == NEG_INF ? 0.f : 1.f / l;
+      const uint64_t inv2 = pair(inv, inv), zero2 = pair(0.f, 0.f);
+      // o / l; what is not finite in the sum (an infinite value, whatever its weight) becomes NaN
+      auto normal = [&](const uint32_t* x) {
+        const uint64_t v = pair(__uint_as_float(x[0]), __uint_as_float(x[1]));
+        return split(fma2(v, zero2, mul2(v, inv2)));
+      };
       const int64_t at = static_cast<int64_t>(w.row0 + r) * H + h + (w.duo ? a : 0);
 #pragma unroll 1
       for (int c = 0; c < 4; c += 2) {
@@ -669,7 +683,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int u = 0; u < 8; ++u) {
             uint32_t v[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = __float_as_uint(__uint_as_float(o[u >> 2][8 * (u & 3) + e]) * inv);
+            for (int e = 0; e < 8; e += 2) {
+              const float2 y = normal(&o[u >> 2][8 * (u & 3) + e]);
+              v[e] = __float_as_uint(y.x);
+              v[e + 1] = __float_as_uint(y.y);
+            }
             store_32(to + 8 * u, v);
           }
         } else if (r < w.rows) {
@@ -678,8 +696,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t* x = &o[u >> 1][16 * (u & 1)];
             uint32_t v[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              v[e] = pack_bf16(__uint_as_float(x[2 * e]) * inv, __uint_as_float(x[2 * e + 1]) * inv);
+            for (int e = 0; e < 8; ++e) {
+              const float2 y = normal(x + 2 * e);
+              v[e] = pack_bf16(y.x, y.y);
+            }
             store_32(p.out + at * 128 + 32 * c + 16 * u, v);
           }
         }
@@ -688,7 +708,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (r < w.rows) {
         const float lse2 = l == 0.f ? NEG_INF : m + log2f(l);
         if (SPLIT) {
-          p.part_lse[part_rows * H + at] = lse2;
+          p.part_lse[part_rows * H + at] = lse2 == NEG_INF ? kNoWeight : lse2;
         } else if (p.lse != nullptr) {
           p.lse[at] = lse2 * kLn2;
         }
@@ -717,7 +737,7 @@ __global__ void __launch_bounds__(256) expanded_merge_kernel(const ExpandedMlaPa
   for (int i = lane; i < p.splits; i += 32) m = fmaxf(m, p.part_lse[i * all + row]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  const float ref = m == NEG_INF ? 0.f : m;
+  const float ref = m <= kNoWeight ? 0.f : m;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   float sum = 0.f;
 #pragma unroll 4

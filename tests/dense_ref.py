@@ -130,3 +130,36 @@ def check(out, lse, exact, rows):
     assert (dz <= e + 2.0 ** -20 * (1 + z.abs())).all(), f"lse {dz.max()}"
     # rows behind the last sequence are left as they were
     assert (out[rows:] == 7.0).all() and (lse[rows:] == 7.0).all()
+
+
+def _definition(q, k, v, scale):
+    """One row in 64 bits over the keys it sees, every product taken (0 x inf too): out, lse."""
+    x = (q * k).sum(-1) * scale
+    p = torch.softmax(x, -1)
+    return (p[:, None] * v).sum(0), torch.logsumexp(x, -1)
+
+
+def compare_nonfinite(c, out, lse, keys_values):
+    """Values or keys that are not finite: NaN exactly where it has to be, and the roundings' 2-norm over the rest;
+    keys_values(b, h) -> keys, values of head h.  Returns how many outputs are NaN."""
+    row, err, ref, nan_dims = 0, 0.0, 0.0, 0
+    for b, (n, kv) in enumerate(zip(c.q_len, c.kv_len)):
+        for i in range(n):
+            see = kv - n + i + 1
+            for h in range(c.heads):
+                k, v = keys_values(b, h)
+                want, z = _definition(c.q[row, h].double(), k[:see], v[:see], c.scale)
+                got = out[row, h].double()
+                bad = ~torch.isfinite(want)          # an infinite value of weight > 0 is NaN too
+                assert torch.equal(torch.isnan(got), bad), (row, h, torch.isnan(got).sum(), bad.sum())
+                assert torch.isfinite(got[~bad]).all()
+                err += float((got - want)[~bad].square().sum())
+                ref += float(want[~bad].square().sum())
+                if torch.isfinite(z):
+                    assert abs(float(lse[row, h]) - float(z)) <= 1e-3 * (1 + abs(float(z)))
+                else:
+                    assert torch.isnan(lse[row, h]) or not bad.all()
+                nan_dims += int(bad.sum())
+            row += 1
+    assert err ** 0.5 <= 2.0 ** -8 * ref ** 0.5
+    return nan_dims
