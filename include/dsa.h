@@ -295,7 +295,10 @@ DSA_API dsa_status_t dsa_sparse_mla_no_alloc(const dsa_batch_t* batch, const voi
  * in fp32, probabilities rounded to bf16 for the second product (relative
  * 2^-8 each at most), one rounding to bf16 at the end.
  * What no row sees does not reach the result, whatever it holds: cache rows behind a
- * sequence's kv_len may be NaN.  Rows of q behind cu_q[num_seqs] (a batch
+ * sequence's kv_len may be NaN.  Of what a row does see, a value c[s][d] that is not
+ * finite makes output d NaN and a NaN score or one of +inf the whole row; a key
+ * of score -inf has weight 0, and a row of only such keys gets out = 0, lse = -inf.
+ * Rows of q behind cu_q[num_seqs] (a batch
  * padded to a captured token count) are left as they were in out and lse.
  * A sequence whose descriptors address rows outside the cache (q_len > kv_len,
  * kv_len > max_kv_len, kv_start + kv_len > total_keys) records
@@ -334,10 +337,8 @@ DSA_API dsa_status_t dsa_prefix_mla(const dsa_batch_t* batch, int32_t prefix_len
  *   DSA_ERR_UNSUPPORTED: the expanded rows are made for the call).
  *   ws of DSA_OP_EXPANDED_MLA bytes.
  * Arithmetic, masked positions, rows behind the last sequence and bad descriptors (q_len >
- * max_q_per_seq among them) as dsa_dense_mla.  Of what a row does see, a value that
- * is not finite (infinities too) makes that output NaN, a NaN score or one of +inf the
- * whole row; a key of score -inf has weight 0, and a row of only such keys gets out = 0,
- * lse = -inf. */
+ * max_q_per_seq among them) as dsa_dense_mla; a value that is not finite (infinities
+ * too) and that a row does see makes that output NaN. */
 DSA_API dsa_status_t dsa_expanded_mla(const dsa_batch_t* batch, const void* q, int32_t n_heads, const void* kv_up,
                                       const void* rope, int64_t rope_stride, float sm_scale, void* out, float* lse,
                                       void* ws, size_t ws_bytes, dsa_stream_t stream);

@@ -39,6 +39,8 @@ struct Item {
   int32_t pieces;       // pieces of the item (set where begins), 0: a sequence that is out of range
   int32_t begins;
   int32_t prefix;       // an item of the shared prefix
+  int32_t b;            // sequence (block-table row), and of a flat cache its first row
+  int32_t kstart;
 };
 
 __device__ __forceinline__ float exp2_approx(float x) {
@@ -354,6 +356,8 @@ struct Walk {
       it.base = e.kv - e.q_len;
       it.lo = e.lo;
       it.prefix = e.prefix ? 1 : 0;
+      it.b = e.b;
+      it.kstart = static_cast<int>(e.kstart);
       it.begins = begins ? 1 : 0;
       it.pieces = 0;
       it.last = -1;
@@ -374,13 +378,47 @@ struct Walk {
   }
 };
 
+// An infinite cache value whose product with q is -inf gives its key the weight 0, and 0 x
+// infinity is NaN in the value's dim for every row that sees the key.  The second product shows
+// that by itself but for the positions that the border's cleaning has zeroed although some
+// rows of the item see them: behind the first row's last, up to the last row's.  Where the
+// cleaning met such a value, the item's epilogue looks it up and overwrites the rows' outputs
+// in its dim.
+struct Hidden {
+  int first, last;      // those positions in the item's tiles
+};
+__device__ __forceinline__ Hidden hidden(const Item& it, int min_lim) {
+  return {max(min_lim + 1, it.tile0 * kTile), min(it.last, (it.tile0 + it.n_tiles) * kTile - 1)};
+}
+
+// NaN into the outputs (fp32 if there are any, else bf16; row n at + n * 512) of the rows that see such a
+// value: row n sees positions up to base + (row + n) / heads.  Not inlined: nearly never called.
+static __device__ __noinline__ void write_nan(PageTable pt, const uint16_t* kv, int b, int kstart, Hidden h, int rows,
+                                              int base, int row, int heads, float* dst32, uint16_t* dst16, int t,
+                                              int threads) {
+  for (int d = t; d < 512; d += threads)
+    for (int s = h.first; s <= h.last; ++s) {
+      const int64_t at = cache_row(pt, b, kstart, s);
+      if (at < 0 || (kv[at * 576 + d] & 0x7F80u) != 0x7F80u) continue;
+      for (int n = max((s - base) * heads - row, 0); n < rows; ++n) {      // the rows that see position s
+        if (dst32 != nullptr) {
+          dst32[static_cast<int64_t>(n) * 512 + d] = __int_as_float(0x7FFFFFFF);
+        } else {
+          dst16[static_cast<int64_t>(n) * 512 + d] = 0x7FFFu;
+        }
+      }
+      break;      // later positions are seen by fewer rows
+    }
+}
+
 // Where row n of an item's log-sum-exp (log2 units) goes, and the item's record.
 __device__ __forceinline__ void store_lse(const DenseMlaParams& p, const Item& it, int N, int n, float lse2) {
   const int64_t rows = static_cast<int64_t>(p.total_q) * p.n_heads, r = it.row0 + n;
+  const float piece = lse2 == __int_as_float(0xff800000) && it.n_tiles > 0 ? kNoWeight : lse2;
   if (it.slot >= 0) {
-    p.part_lse[static_cast<int64_t>(it.slot) * N + n] = lse2;
+    p.part_lse[static_cast<int64_t>(it.slot) * N + n] = piece;
   } else if (p.shared) {
-    p.row_lse[(it.prefix ? 0 : rows) + r] = lse2;
+    p.row_lse[(it.prefix ? 0 : rows) + r] = piece;
   } else if (p.lse != nullptr) {
     p.lse[r] = lse2 * kLn2;
   }

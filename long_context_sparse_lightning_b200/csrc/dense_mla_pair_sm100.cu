@@ -83,6 +83,7 @@ struct Aux {
     float mx[2][2][64];                     // per warpgroup and half of a tile's keys: row maxima / row sums
   };
   float ref[64];                            // the rows' references
+  int32_t lost[2];                          // item parity: 1 + number of an item that hidden values were cleaned out of
 };
 static_assert(sizeof(Aux) <= 2048, "");
 
@@ -111,9 +112,12 @@ __device__ __forceinline__ void exchange_4(uint32_t (&v)[32], uint32_t lane) {
 
 // Keys that some row must not see: 0 x a non-finite value would reach that row, so
 // such values become 0 in the tile.  A row that does see the key has its NaN from
-// the score.  By the 128 threads of a warpgroup; not inlined: its code between a
+// the score, or where that is -inf from the epilogue: *lost is set to `tag` in both CTAs, whose
+// rows take this CTA's dims.  By the 128 threads of a warpgroup; not inlined: its code between a
 // tile's softmax and the next costs the tiles that have no border (16K samples prefix 253 us, so 245).
-__device__ __noinline__ void clean_values(uint8_t* stage, int pos0, int lo, int min_lim, int st) {
+__device__ __noinline__ void clean_values(uint8_t* stage, int pos0, int lo, int min_lim, int last, int32_t* lost, int tag,
+                                          int st) {
+  bool seen = false;
 #pragma unroll 1
   for (int u0 = st; u0 < 8 * kBlk / 16; u0 += 8 * 128) {      // (four loads' latency at once)
     uint4* w = reinterpret_cast<uint4*>(stage) + u0;
@@ -126,8 +130,17 @@ __device__ __noinline__ void clean_values(uint8_t* stage, int pos0, int lo, int 
       for (int q = 0; q < 4; ++q) a[q] = w[256 * q + 128 * g];
 #pragma unroll
       for (int q = 0; q < 4; ++q)
-        if (any_not_finite(a[q])) w[256 * q + 128 * g] = finite_or_zero(a[q]);
+        if (any_not_finite(a[q])) {
+          w[256 * q + 128 * g] = finite_or_zero(a[q]);
+          seen |= pos >= lo && pos <= last;
+        }
     }
+  }
+  if (seen) {
+    const uint32_t at = smem_u32(lost);
+    for (uint32_t r = 0; r < 2; ++r)
+      asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(mapa_shared(at, r)), "r"(tag) : "memory");
+    asm volatile("fence.acq_rel.cluster;" ::: "memory");
   }
 }
 
@@ -165,6 +178,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     mbar_init(&ax->o_full, 1);
     mbar_init(&ax->o_free, 16);
+    ax->lost[0] = ax->lost[1] = 0;
     fence_mbar_init();
     prefetch_tmap(&maps.q);
     prefetch_tmap(&maps.c);
@@ -498,7 +512,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                        "r"(pk[4 * u]), "r"(pk[4 * u + 1]), "r"(pk[4 * u + 2]), "r"(pk[4 * u + 3])
                        : "memory");
         wait(&ax->v_full[s], (t / kStages) & 1, 584);
-        if (border) clean_values(sm + OFF_KV + s * kStage, pos0, it.lo, min_lim, st);
+        if (border) clean_values(sm + OFF_KV + s * kStage, pos0, it.lo, min_lim, it.last, &ax->lost[k & 1], k + 1, st);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive_remote(p_full0 + 8 * (t & 1));
@@ -523,6 +537,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         ++n_o;
         tc_fence_after();
       }
+      // read before o_free, which the item after next, whose flag this will be, waits for
+      const bool lost = *static_cast<volatile int32_t*>(&ax->lost[k & 1]) == k + 1;
       float* dst32 = fp32_rows(p, it, kN);
       // 64 dims at a time.  A thread has a row's, which would go out as 32 rows' sectors an
       // instruction; four lanes exchange theirs first, so that each row gets whole lines (16K
@@ -572,6 +588,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_remote(o_free);
+      }
+      if (lost) {
+        // this CTA's rows of the item, of all dims
+        bar_sync(1, kSoftThreads);    // the outputs are written
+        const int r0 = 64 * static_cast<int>(rank);
+        write_nan(p.pt, p.kv, it.b, it.kstart, hidden(it, min_lim), min(it.rows - r0, 64), it.base,
+                  it.row0 + r0 - it.seq_row0, H, dst32 == nullptr ? nullptr : dst32 + r0 * 512, p.out + static_cast<int64_t>(it.row0 + r0) * 512, tid - 128,
+                  kSoftThreads);
       }
       bar_sync(1, kSoftThreads);      // mx and ref may be rewritten
     }

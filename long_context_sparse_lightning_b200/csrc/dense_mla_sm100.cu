@@ -92,6 +92,7 @@ struct Aux {
   float fac[32];            // rescaling factors, inverse row sums
   float ref[32];            // the rows' references, at the end of an item
   int32_t lim[32];          // last position each row sees
+  int32_t lost;             // hidden values of the item that are not finite were cleaned
 };
 static_assert(sizeof(Aux) <= 2048, "");
 
@@ -121,10 +122,11 @@ __device__ __forceinline__ void ld_cols16(uint32_t t, uint32_t (&r)[16]) {
 
 // Keys that some row must not see: 0 x a non-finite value would reach that row, so
 // such values become 0 in the tile (its pairs are slots n, n + 1, n + 2, n + 3 of the ring).
-// A row that does see the key has its NaN from the score.  By 128 threads; not
-// inlined, to stay out of the tiles that have no border.
+// A row that does see the key has its NaN from the score, or where that is -inf from the
+// epilogue (*lost is set).  By 128 threads; not inlined, to stay out of the tiles that have no border.
 template <int SLOTS>
-__device__ __noinline__ void clean_values(uint8_t* pairs, int n, int pos0, int lo, int min_lim, int st) {
+__device__ __noinline__ void clean_values(uint8_t* pairs, int n, int pos0, int lo, int min_lim, int last, int32_t* lost,
+                                          int st) {
 #pragma unroll 1
   for (int g = 0; g < 4; ++g) {                // key st / 8 + 16 g, eight units of it
     const int pos = pos0 + (st >> 3) + 16 * g;
@@ -135,9 +137,11 @@ __device__ __noinline__ void clean_values(uint8_t* pairs, int n, int pos0, int l
       a[q] = reinterpret_cast<const uint4*>(pairs + (n + (q >> 1)) % SLOTS * kPair + (q & 1) * kBlk)[st + 128 * g];
 #pragma unroll
     for (int q = 0; q < 8; ++q)
-      if (any_not_finite(a[q]))
+      if (any_not_finite(a[q])) {
         reinterpret_cast<uint4*>(pairs + (n + (q >> 1)) % SLOTS * kPair + (q & 1) * kBlk)[st + 128 * g] =
             finite_or_zero(a[q]);
+        if (pos >= lo && pos <= last) *lost = 1;
+      }
   }
 }
 
@@ -387,6 +391,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (it.n_tiles < 0) break;
       if (st < N)
         ax->lim[st] = st >= it.rows ? -1 : (it.prefix ? it.last : it.base + (it.row0 + st - it.seq_row0) / H);
+      if (st == 0) ax->lost = 0;
       bar_sync(1, kSoftThreads);
       const int min_lim = ax->lim[0];       // row 0 is the earliest token's
       float mr[2 * KC], l[2 * KC];
@@ -485,7 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
           for (int m = 0; m < 4; ++m)
             wait(&ax->pair_full[(4 * t + m) % C::PAIR_SLOTS], ((4 * t + m) / C::PAIR_SLOTS) & 1, 534);
-          clean_values<C::PAIR_SLOTS>(sm + C::OFF_PAIR, 4 * t, pos0, it.lo, min_lim, st);
+          clean_values<C::PAIR_SLOTS>(sm + C::OFF_PAIR, 4 * t, pos0, it.lo, min_lim, it.last, &ax->lost, st);
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -564,6 +569,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&ax->o_empty);
+      }
+      if (ax->lost != 0) {
+        bar_sync(1, kSoftThreads);        // the outputs are written
+        write_nan(p.pt, p.kv, it.b, it.kstart, hidden(it, min_lim), it.rows, it.base, it.row0 - it.seq_row0, H, dst32,
+                  p.out + static_cast<int64_t>(it.row0) * 512, st, kSoftThreads);
       }
       bar_sync(1, kSoftThreads);          // fac and lim may be rewritten
     }
@@ -662,7 +672,7 @@ __global__ void __launch_bounds__(256) dense_merge_kernel(const DenseMlaParams p
 #pragma unroll
     for (int c = 0; c < 4; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
     float sum = 0.f;
-    const float ref = m == NEG_INF ? 0.f : m;
+    const float ref = m <= kNoWeight ? 0.f : m;
     for (int j = w0; j < n; j += WARPS) {
       if (j != w0) load(j);
       const float z = j < 32 ? __shfl_sync(0xffffffffu, mine, j) : lse_of(j);
