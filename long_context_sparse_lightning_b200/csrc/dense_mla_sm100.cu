@@ -209,6 +209,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int k = 0, n_q = 0, n_rope = 0, n_pair = 0;
     auto publish = [&](const Item& it) {
       if (k >= 2) wait(&ax->item_free[k & 1], ((k >> 1) + 1) & 1, 510);
+      __syncwarp();      // every lane has its copy of the share, whose memory the softmax warps write from here on
       if (ok && lane == 0) {
         ax->item[k & 1] = it;
         mbar_arrive(&ax->item_full[k & 1]);
