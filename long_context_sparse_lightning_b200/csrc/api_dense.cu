@@ -94,6 +94,7 @@ dsa_status_t run_dense(const dsa_batch_t* b, int prefix_len, const void* q, int 
   p.row_o = reinterpret_cast<float*>(base + l.row_o);
   p.err = reinterpret_cast<uint32_t*>(base);
   p.budget = dsa::wait_budget();
+  p.skip_arrival = dsa::test_skip_arrival();
   const bool pair = d.n == 128;
   const uint64_t rows = static_cast<uint64_t>(b->total_q) * n_heads, keys = static_cast<uint64_t>(b->total_keys);
   dsa::DenseMaps maps;
@@ -166,6 +167,7 @@ dsa_status_t dsa_expanded_mla(const dsa_batch_t* b, const void* q, int32_t n_hea
   p.lse = lse;
   p.err = static_cast<uint32_t*>(ws);
   p.budget = dsa::wait_budget();
+  p.skip_arrival = dsa::test_skip_arrival();
   const uint64_t h = static_cast<uint64_t>(n_heads);
   CUtensorMap map_q, map_kv, map_r;
   if (!dsa::make_tmap_blocks(&map_q, q, static_cast<uint64_t>(b->total_q), h * 3, h * 192, 128, 3) ||

@@ -75,6 +75,7 @@ struct Aux {
   uint64_t ref_set[2];                      // tile parity: the rows' references with the tile are known
   uint64_t o_full, o_free;
   uint64_t item_full[2], item_free[2];
+  uint64_t drain;
   Item item[2];
   int32_t row[kStages];                     // cache row of the tile's position 0, -1: a page outside the pool
   uint32_t tmem;
@@ -176,6 +177,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(&ax->ref_set[i], 4);
       mbar_init(&ax->item_free[i], rank == 0 ? 10 : 9); // softmax warps, warp 2, rank 0's MMA thread
     }
+    mbar_init(&ax->drain, 1);
     mbar_init(&ax->o_full, 1);
     mbar_init(&ax->o_free, 16);
     ax->lost[0] = ax->lost[1] = 0;
@@ -271,7 +273,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       end.n_tiles = -1;
       publish(end);
     }
-    if (!ok) drain_pause();      // a wait ran out: the copies in flight land before the blocks end
+    // All copies land before the blocks end, also those that nothing waits for any more because a
+    // wait has run out, here or in another role.  Rank 0's barriers count both CTAs'; what rank 1
+    // has issued beyond rank 0 lands within its pause.
+    bool landed = rank == 0;
+    if (landed && n_q > 0) landed = mbar_wait(&ax->q_full, (n_q - 1) & 1, kDrainCycles);
+    for (int i = max(0, t - kStages); landed && i < t; ++i)
+      landed = mbar_wait(&ax->full[i % kStages], (i / kStages) & 1, kDrainCycles);
+    if (!ok && rank != 0) drain_pause();
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMAs --
     if (rank == 0 && elect_one()) {
@@ -339,7 +348,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         ++n_o;
       }
-      if (!ok) drain_pause();      // the MMAs in flight, before their memory goes
+      // the MMAs in flight end before their memory goes, whichever role has given up
+      umma_commit_pair_here(&ax->drain);
+      mbar_wait(&ax->drain, 0, kDrainCycles);
     }
   } else if (warp == 2) {
     // ------------------------- the other CTA's keys at this CTA's dims by TMA --
@@ -381,7 +392,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         __syncwarp();
       }
     }
-    if (!ok) drain_pause();
+    bool landed = true;
+    for (int i = max(0, n_own - kStages); landed && i < n_own; ++i)
+      landed = mbar_wait(&ax->v_full[i % kStages], (i / kStages) & 1, kDrainCycles);
   } else if (warp >= 4) {
     // ---------------------------------------------------- softmax, epilogue --
     // The two warpgroups take turns at the tiles: one alone, a warp per scheduler,
@@ -587,15 +600,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (it.n_tiles > 0) {
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_remote(o_free);
+        if (lane == 0 && !(unit == 0 && n_o - 1 == p.skip_arrival)) mbar_arrive_remote(o_free);
       }
       if (lost) {
         // this CTA's rows of the item, of all dims
         bar_sync(1, kSoftThreads);    // the outputs are written
         const int r0 = 64 * static_cast<int>(rank);
         write_nan(p.pt, p.kv, it.b, it.kstart, hidden(it, min_lim), min(it.rows - r0, 64), it.base,
-                  it.row0 + r0 - it.seq_row0, H, dst32 == nullptr ? nullptr : dst32 + r0 * 512, p.out + static_cast<int64_t>(it.row0 + r0) * 512, tid - 128,
-                  kSoftThreads);
+                  it.row0 + r0 - it.seq_row0, H, dst32 == nullptr ? nullptr : dst32 + r0 * 512,
+                  p.out + static_cast<int64_t>(it.row0 + r0) * 512, tid - 128, kSoftThreads);
       }
       bar_sync(1, kSoftThreads);      // mx and ref may be rewritten
     }

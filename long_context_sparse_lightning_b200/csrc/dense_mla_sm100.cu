@@ -273,15 +273,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       end.n_tiles = -1;
       publish(end);
     }
-    if (!ok) {
-      // a wait ran out: let the copies in flight land before the block ends
-      bool landed = true;
-      if (n_q > 0) landed = mbar_wait(&ax->q_full, (n_q - 1) & 1, kDrainCycles) && landed;
-      for (int i = max(0, n_rope - C::ROPE_SLOTS); landed && i < n_rope; ++i)
-        landed = mbar_wait(&ax->rope_full[i % C::ROPE_SLOTS], (i / C::ROPE_SLOTS) & 1, kDrainCycles);
-      for (int i = max(0, n_pair - C::PAIR_SLOTS); landed && i < n_pair; ++i)
-        landed = mbar_wait(&ax->pair_full[i % C::PAIR_SLOTS], (i / C::PAIR_SLOTS) & 1, kDrainCycles);
-    }
+    // All copies land before the block ends, also those that nothing waits for any more because
+    // a wait has run out, here or in another role.
+    bool landed = true;
+    if (n_q > 0) landed = mbar_wait(&ax->q_full, (n_q - 1) & 1, kDrainCycles);
+    for (int i = max(0, n_rope - C::ROPE_SLOTS); landed && i < n_rope; ++i)
+      landed = mbar_wait(&ax->rope_full[i % C::ROPE_SLOTS], (i / C::ROPE_SLOTS) & 1, kDrainCycles);
+    for (int i = max(0, n_pair - C::PAIR_SLOTS); landed && i < n_pair; ++i)
+      landed = mbar_wait(&ax->pair_full[i % C::PAIR_SLOTS], (i / C::PAIR_SLOTS) & 1, kDrainCycles);
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMAs --
     if (elect_one()) {
@@ -353,10 +352,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         ++n_o;
       }
-      if (!ok) {
-        umma_commit(&ax->drain);
-        mbar_wait(&ax->drain, 0, kDrainCycles);
-      }
+      // the MMAs in flight end before their memory goes, whichever role has given up
+      umma_commit(&ax->drain);
+      mbar_wait(&ax->drain, 0, kDrainCycles);
     }
   } else {
     // ---------------------------------------------------- softmax, epilogue --
@@ -569,7 +567,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (it.n_tiles > 0) {
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&ax->o_empty);
+        if (lane == 0 && !(blockIdx.x == 0 && n_o - 1 == p.skip_arrival)) mbar_arrive(&ax->o_empty);
       }
       if (ax->lost != 0) {
         bar_sync(1, kSoftThreads);        // the outputs are written

@@ -382,14 +382,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           values(i);
           if (ok && i + 1 < n_tiles) keys(i + 1);
         }
-        if (!ok) {      // let the copies in flight land before the block ends
-          bool landed = true;
-          for (int a = 0; a < (two ? 2 : 1); ++a) landed = landed && mbar_wait(&ax->q_full[a], 0, kDrainCycles);
-          for (int i = max(0, n_k - 2); landed && i < n_k; ++i)
-            landed = mbar_wait(&ax->k_full[i & 1], (i >> 1) & 1, kDrainCycles);
-          for (int i = max(0, n_v - 2); landed && i < n_v; ++i)
-            landed = mbar_wait(&ax->v_full[i & 1], (i >> 1) & 1, kDrainCycles);
-        }
+        // all copies land before the block ends, also those that nothing waits for any more
+        // because a wait has run out, here or in another role
+        bool landed = true;
+        for (int a = 0; a < (two ? 2 : 1); ++a) landed = landed && mbar_wait(&ax->q_full[a], 0, kDrainCycles);
+        for (int i = max(0, n_k - 2); landed && i < n_k; ++i)
+          landed = mbar_wait(&ax->k_full[i & 1], (i >> 1) & 1, kDrainCycles);
+        for (int i = max(0, n_v - 2); landed && i < n_v; ++i)
+          landed = mbar_wait(&ax->v_full[i & 1], (i >> 1) & 1, kDrainCycles);
       }
     } else if (warp == 1) {
       // ---------------------------------------------------------------- MMAs --
@@ -458,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; ok && i < n_tiles; ++i) {
           wait(&ax->v_full[i & 1], (i >> 1) & 1, 624);
-          if (i + 1 == border0) mbar_arrive(&ax->go);
+          if (i + 1 == border0 && p.skip_arrival < 0) mbar_arrive(&ax->go);
           if (i >= border0) wait(&ax->clean[(i - border0) & 1], ((i - border0) >> 1) & 1, 623);
           if (w.duo) {
             // One head's product each; the next keys land over tiles that are done, so the next
@@ -486,10 +486,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        if (!ok) {
-          umma_commit(&ax->drain);
-          mbar_wait(&ax->drain, 0, kDrainCycles);
-        }
+        // the MMAs in flight end before their memory goes, whichever role has given up
+        umma_commit(&ax->drain);
+        mbar_wait(&ax->drain, 0, kDrainCycles);
       }
     } else {
       // -------------------------------------------- value tiles on the border --

@@ -88,7 +88,8 @@ struct IndexerParams {
                               // release of this accumulator item (see test_skip_arrival)
 };
 
-// Item whose accumulator release CTA (0,0,0) of the indexer skips, so that a
+// Item whose accumulator release CTA (0,0,0) of the indexer skips (or the first
+// CTA of a dense attention; see their parameters), so that a
 // bounded wait runs out: DSA_TEST_SKIP_ARRIVAL, read per call; -1 (unset) in
 // normal use.  For tests of the device error path only.
 int test_skip_arrival();
@@ -233,6 +234,8 @@ struct DenseMlaParams {
   float* row_o = nullptr;             // shared: [2, total_q * H, 512]
   uint32_t* err = nullptr;
   long long budget = 2000000000LL;
+  int32_t skip_arrival = -1;          // failure-path tests only: the first CTA (pair) withholds the release of its
+                                      // accumulator behind this item (see test_skip_arrival)
 };
 constexpr int kDenseMaxCtas = 148;
 // Partial slots: two per unit (a CTA, or a CTA pair for N = 128).
@@ -280,6 +283,8 @@ struct ExpandedMlaParams {
   float* part_o = nullptr;            // splits > 1: [splits, total_q, H, 128] normalised
   uint32_t* err = nullptr;
   long long budget = 2000000000LL;
+  int32_t skip_arrival = -1;          // failure-path tests only, >= 0: the MMA threads withhold the arrival
+                                      // that lets the cleaning warps start (see test_skip_arrival)
 };
 // Parts for a batch: 1 unless its row tiles leave half of the SMs idle.
 int expanded_splits(const dsa_batch_t* b, int n_heads);

@@ -137,12 +137,12 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity
   return true;
 }
 
-// After a wait has run out: time for what is still in flight (copies into shared
-// memory, MMAs) to finish before the block ends, whatever the wait budget is.
+// Before a block ends: time for what may still be in flight after a wait has run out (copies
+// into shared memory, MMAs) to finish, whatever the wait budget is.
 constexpr long long kDrainCycles = 1LL << 22;      // ~2 ms, for waits on barriers
-__device__ __forceinline__ void drain_pause() {    // where there is no barrier to wait on: ~0.1 ms
+__device__ __forceinline__ void drain_pause() {    // the same where there is no barrier of this CTA's to wait on
   const long long t0 = clock64();
-  while (clock64() - t0 < 200000) __nanosleep(1000);
+  while (clock64() - t0 < kDrainCycles) __nanosleep(1000);
 }
 
 // ----------------------------------------------------------------------------
@@ -237,6 +237,11 @@ __device__ __forceinline__ void umma_commit_pair(uint64_t* bar) {
           smem_u32(bar)),
       "h"(static_cast<uint16_t>(3))
       : "memory");
+}
+// The same on this CTA's barrier alone.
+__device__ __forceinline__ void umma_commit_pair_here(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+               : "memory");
 }
 // 3-D tiled load into this CTA's shared memory that signals a barrier of either
 // CTA of the pair (cluster address from mapa).

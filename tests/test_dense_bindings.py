@@ -36,8 +36,9 @@ def test_from_requests_allocates_on_the_stream_that_writes(monkeypatch):
     monkeypatch.setattr(dsa, "page_tables", lambda *a: launched.append(a[-1]))
     for stream in (None, "side"):
         seen.clear()
-        batch, pos, slots, used = dsa.Batch.from_requests(ints(2, 1), ints(0, 5), ints(3, 4), 64, torch.zeros((2, 2), dtype=torch.int32),
-                                                          torch.zeros(256, dtype=torch.uint8), 4, 2, 6, 320, stream)
+        batch, pos, slots, used = dsa.Batch.from_requests(
+            ints(2, 1), ints(0, 5), ints(3, 4), 64, torch.zeros((2, 2), dtype=torch.int32),
+            torch.zeros(256, dtype=torch.uint8), 4, 2, 6, 320, stream)
         assert seen == [stream] * 5 and launched[-1] == stream and not inside
         assert batch.total_q == 4 and pos.numel() == slots.numel() == 4 and used.numel() == 1
 
