@@ -139,8 +139,8 @@ typedef struct {
  * (which do not read k_sel) hold their partial results there: up to 39 MB for
  * DSA_OP_DENSE_MLA and 16 bytes a row, plus 4 KB a row (query token and
  * head) for DSA_OP_PREFIX_MLA; for DSA_OP_EXPANDED_MLA 516 bytes a row and key
- * split where the rows of the batch's bounds alone would leave SMs idle, else
- * 256 bytes (so a smaller batch may need more than a larger one). */
+ * split, up to 20 MB, where contexts are long enough to be split, else 256 bytes.
+ * Their sizes serve every batch of the same n_heads within this one's bounds. */
 DSA_API size_t dsa_workspace_size(dsa_op_t op, const dsa_batch_t* batch, int32_t k_sel, int32_t n_heads);
 
 /* Indexer scores.

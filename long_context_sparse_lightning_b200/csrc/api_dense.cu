@@ -42,10 +42,10 @@ struct ExpandedLayout {
   size_t part_lse, part_o, bytes;
 };
 
-ExpandedLayout expanded_layout(const dsa_batch_t* b, int n_heads) {
+ExpandedLayout expanded_layout(int splits, int64_t total_q, int n_heads) {
   ExpandedLayout l;
-  l.splits = dsa::expanded_splits(b, n_heads);
-  const size_t rows = l.splits > 1 ? static_cast<size_t>(l.splits) * b->total_q * n_heads : 0;
+  l.splits = splits;
+  const size_t rows = splits > 1 ? static_cast<size_t>(splits) * static_cast<size_t>(total_q) * n_heads : 0;
   l.part_lse = kHeader;
   l.part_o = l.part_lse + round_up(rows * sizeof(float), 256);
   l.bytes = l.part_o + rows * 128 * sizeof(float);
@@ -116,7 +116,14 @@ size_t dense_ws_bytes(const dsa_batch_t* b, int n_heads, bool shared) {
 
 size_t expanded_ws_bytes(const dsa_batch_t* b, int n_heads) {
   if (n_heads < 1 || n_heads > 128 || b->block_table != nullptr) return 0;
-  return expanded_layout(b, n_heads).bytes;
+  // enough for every batch within this one's bounds: those of fewer rows are split into more parts
+  size_t most = kHeader;
+  for (int s = 2; s <= dsa::expanded_most_splits(b->max_kv_len, n_heads); ++s) {
+    const int64_t fit = dsa::kExpandedPartRows / (s * n_heads);
+    const size_t bytes = expanded_layout(s, b->total_q < fit ? b->total_q : fit, n_heads).bytes;
+    if (bytes > most) most = bytes;
+  }
+  return most;
 }
 }  // namespace dsa
 
@@ -146,7 +153,7 @@ dsa_status_t dsa_expanded_mla(const dsa_batch_t* b, const void* q, int32_t n_hea
   if (!(sm_scale > 0.f) || !std::isfinite(sm_scale)) return DSA_ERR_INVALID_ARG;
   if (n_heads < 1 || n_heads > 128 || b->block_table != nullptr) return DSA_ERR_UNSUPPORTED;
   if (ws == nullptr || misaligned(ws, 16)) return DSA_ERR_INVALID_ARG;
-  const ExpandedLayout l = expanded_layout(b, n_heads);
+  const ExpandedLayout l = expanded_layout(dsa::expanded_splits(b, n_heads), b->total_q, n_heads);
   if (ws_bytes < l.bytes) return DSA_ERR_WORKSPACE;
   if (b->total_q == 0) return DSA_OK;
   dsa::ExpandedMlaParams p;

@@ -761,12 +761,18 @@ __global__ void __launch_bounds__(256) expanded_merge_kernel(const ExpandedMlaPa
 
 }  // namespace
 
+int expanded_most_splits(int max_kv_len, int n_heads) {
+  const int tiles = (max_kv_len + kKeys - 1) / kKeys, s = kDenseMaxCtas / n_heads;
+  return s < tiles / kSplitTiles ? s : (tiles / kSplitTiles > 1 ? tiles / kSplitTiles : 1);
+}
+
 int expanded_splits(const dsa_batch_t* b, int n_heads) {
-  const int64_t ctas = static_cast<int64_t>((b->max_q_per_seq + 2 * kRows - 1) / (2 * kRows)) * n_heads * b->num_seqs;
-  if (ctas < 1 || ctas > kDenseMaxCtas / 2) return 1;
-  const int tiles = (b->max_kv_len + kKeys - 1) / kKeys;
-  const int64_t s = kDenseMaxCtas / ctas;
-  return static_cast<int>(s < tiles / kSplitTiles ? s : (tiles / kSplitTiles > 1 ? tiles / kSplitTiles : 1));
+  const int64_t units = static_cast<int64_t>((b->max_q_per_seq + 2 * kRows - 1) / (2 * kRows)) * b->num_seqs;
+  const int64_t ctas = units * n_heads, rows = static_cast<int64_t>(b->total_q) * n_heads;
+  if (ctas < 1 || ctas > kDenseMaxCtas / 2 || rows < 1) return 1;
+  const int64_t s = kDenseMaxCtas / ctas, fit = kExpandedPartRows / rows, most = expanded_most_splits(b->max_kv_len, n_heads);
+  const int64_t least = s < fit ? (s < most ? s : most) : (fit < most ? fit : most);
+  return static_cast<int>(least > 1 ? least : 1);
 }
 
 cudaError_t launch_expanded_mla(const ExpandedMlaParams& p, const CUtensorMap& map_q, const CUtensorMap& map_kv,

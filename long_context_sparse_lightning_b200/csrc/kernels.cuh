@@ -286,8 +286,13 @@ struct ExpandedMlaParams {
   int32_t skip_arrival = -1;          // failure-path tests only, >= 0: the MMA threads withhold the arrival
                                       // that lets the cleaning warps start (see test_skip_arrival)
 };
-// Parts for a batch: 1 unless its row tiles leave half of the SMs idle.
+// Parts for a batch: 1 unless its row tiles leave half of the SMs idle.  The partial results are
+// kept for rows x parts <= kExpandedPartRows, a row tile of every SM: a bound that only a total_q
+// padded beyond what its sequences can hold meets.
+constexpr int kExpandedPartRows = kDenseMaxCtas * 256;
 int expanded_splits(const dsa_batch_t* b, int n_heads);
+// The most parts of any batch of sequences up to max_kv_len.
+int expanded_most_splits(int max_kv_len, int n_heads);
 // Descriptors (see make_tmap_blocks) of q as [total_q, H * 192], boxes of 3 x 128;
 // kv_up as [total_keys, H * 256] and the RoPE dims [total_keys, 64], boxes of 1 x 128.
 cudaError_t launch_expanded_mla(const ExpandedMlaParams& p, const CUtensorMap& map_q, const CUtensorMap& map_kv,

@@ -2,6 +2,8 @@
 device a call's memory and work belong to, and arrays that must not reach a kernel."""
 
 import contextlib
+import ctypes
+import random
 
 import pytest
 import torch
@@ -108,3 +110,31 @@ def test_errors_are_read_behind_the_stream_of_the_workspaces_device(monkeypatch)
     assert seen == [(4096, 1000), (4096, 77)]
     with pytest.raises(ValueError, match="CUDA"):
         dsa.check_device_error(torch.zeros(256, dtype=torch.uint8))
+
+
+def test_a_workspace_serves_every_smaller_batch():
+    # a serving loop allocates once, for its bounds: fewer rows over long contexts are split into more parts
+    lib, rng = dsa.library(), random.Random(1)
+
+    def size(op, heads, B, total_q, max_q, max_kv):
+        c = dsa._BatchC()
+        c.num_seqs, c.total_q, c.max_q_per_seq, c.max_kv_len, c.total_keys = B, total_q, max_q, max_kv, 1 << 20
+        c.cu_q = c.kv_len = c.block_table = 0x1000
+        c.page_size, c.blocks_per_seq = 64, 1 << 14
+        if op == dsa.OP_EXPANDED_MLA:
+            c.block_table, c.kv_start = None, 0x1000
+        return lib.dsa_workspace_size(op, ctypes.byref(c), 0, heads)
+
+    for _ in range(2000):
+        heads = rng.choice([1, 2, 16, 20, 70, 128])
+        total_q = rng.choice([1, 10, 300, 8192, 40000])
+        big = (rng.choice([1, 2, 8, 500]), total_q, rng.randint(1, total_q), 0)
+        big = big[:3] + (max(big[2], rng.choice([1, 700, 3000, 100000])),)
+        small = (rng.randint(1, big[0]), rng.randint(1, big[1]))
+        small += (rng.randint(1, min(small[1], big[2])),)
+        small += (rng.randint(small[2], big[3]),)
+        for op in (dsa.OP_DENSE_MLA, dsa.OP_PREFIX_MLA, dsa.OP_EXPANDED_MLA):
+            need, have = size(op, heads, *small), size(op, heads, *big)
+            assert 0 < need <= have, (op, heads, small, big)
+            if op == dsa.OP_EXPANDED_MLA:
+                assert have <= 20 << 20

@@ -1,10 +1,12 @@
-"""The bindings of the dense attentions and the page tables on a GPU: a batch made on another
-stream than the current one."""
+"""The bindings of the dense attentions and the page tables on a GPU: a batch made on another stream
+than the current one, one workspace for steps of different sizes."""
 
 import pytest
 import torch
 
 import long_context_sparse_lightning_b200 as dsa
+from tests.dense_ref import check
+from tests.test_gpu_expanded_mla import Expanded
 
 pytestmark = pytest.mark.gpu
 
@@ -27,3 +29,16 @@ def test_from_requests_on_another_stream_leaves_freed_memory_of_the_current_one(
     assert batch.cu_q.tolist() == [0, 2, 3] and batch.kv_len.tolist() == [2, 65] and used.tolist() == [2]
     assert pos.tolist() == [0, 1, 64, 0] and slots.tolist() == [320, 321, 384, -1]
     dsa.check_device_error(ws, side)
+
+
+def test_expanded_steps_in_one_workspace_of_the_largest():
+    # prompts, then few rows over long contexts (split keys), then a step padded far beyond its sequences
+    steps = [([700, 300], [700, 900], 0), ([1], [5000], 0), ([40], [2600], 0), ([3, 2], [2000, 900], 700)]
+    cases = [Expanded(q, kv, 16, seed=41 + i, pad_rows=pad) for i, (q, kv, pad) in enumerate(steps)]
+    bounds = dsa.Batch(cases[0].cu_q, cases[0].kv, cases[0].start, 1000, 700, 5000, 5000)
+    ws = dsa.workspace(dsa.OP_EXPANDED_MLA, bounds, n_heads=16)
+    for c in cases:
+        out, lse = c.outputs(128)
+        dsa.expanded_mla(c.batch, c.q.cuda(), c.up.cuda(), c.cache.cuda()[:, 512:], c.scale, out, lse, ws)
+        dsa.check_device_error(ws)
+        check(out.cpu(), lse.cpu(), c.exact_expanded(), c.rows)
