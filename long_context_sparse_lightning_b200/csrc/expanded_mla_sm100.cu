@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int kv = __ldg(&p.kv_len[b]);
   const int64_t ks = __ldg(&p.kv_start[b]);
   Tile w;
-  w.bad = q_len > kv || q_len > p.max_q || kv > p.max_kv_len || ks < 0 || ks + kv > p.total_keys;
+  w.bad = q_len > kv || q_len > p.max_q || kv > p.max_kv_len || ks < 0 || ks > p.total_keys - kv;
   w.row0 = q0 + qt * 2 * kRows;
   w.rows = q_len - qt * 2 * kRows;       // rows behind the last tile's are the last tile's where max_q is too small
   if (w.rows > 2 * kRows && !(w.bad && qt == p.row_tiles - 1)) w.rows = 2 * kRows;

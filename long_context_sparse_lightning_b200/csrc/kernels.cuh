@@ -43,7 +43,7 @@ __device__ __forceinline__ int64_t seq_start(const PageTable& pt, const int64_t*
 // Every position 0 .. kv-1 of the sequence has a cache row: inside the flat
 // cache, or inside the sequence's block-table row.
 __device__ __forceinline__ bool seq_rows_ok(const PageTable& pt, int64_t kstart, int kv, int64_t total_keys) {
-  if (pt.table == nullptr) return kstart >= 0 && kstart + kv <= total_keys;
+  if (pt.table == nullptr) return kstart >= 0 && kstart <= total_keys - kv;      // (the sum may overflow)
   return static_cast<int64_t>(kv) <= static_cast<int64_t>(pt.stride) * pt.page;
 }
 

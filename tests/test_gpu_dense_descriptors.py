@@ -76,7 +76,7 @@ def test_a_page_of_the_shared_prefix_outside_the_pool_is_skipped(heads):
 
 
 @pytest.mark.parametrize("heads", HEADS)
-@pytest.mark.parametrize("what", ["start", "negative start", "kv_len", "too long", "negative kv_len"])
+@pytest.mark.parametrize("what", ["start", "negative start", "last start", "kv_len", "too long", "negative kv_len"])
 def test_a_sequence_outside_the_cache_is_zero(heads, what):
     for make, run, dim in ((lambda: Case([2, 2, 1], [200, 300, 100], heads, 0, seed=53), dense, 512),
                            (lambda: Expanded([2, 2, 1], [200, 300, 100], heads, seed=53), expanded, 128)):
@@ -86,6 +86,8 @@ def test_a_sequence_outside_the_cache_is_zero(heads, what):
             c.start[1] = c.total_keys - 299
         elif what == "negative start":
             c.start[1] = -1
+        elif what == "last start":
+            c.start[1] = 2 ** 63 - 1         # its sum with a length overflows
         else:
             c.kv[1] = {"kv_len": 1, "too long": 301, "negative kv_len": -5}[what]
         out, lse = run(c)
@@ -115,3 +117,24 @@ def test_offsets_that_do_not_rise_where_blocks_look_up_their_row_tile():
     out, _ = expanded(c)
     keep = [r for r in range(c.rows) if not 600 + 3 * 3 <= r < 600 + 5 * 3]
     near(out[:c.rows][keep], want[keep])
+
+
+def test_a_first_row_whose_sum_with_the_length_overflows():
+    # the same descriptor in the library's other calls: an error, and not an address far outside
+    c = Case([2, 2], [200, 300], 16, 0, seed=56)
+    c.start[0] = 2 ** 63 - 1
+    ws = dsa.workspace(dsa.OP_FORWARD, c.batch, 64, 16)
+    idx = torch.arange(64, dtype=torch.int32, device="cuda").repeat(4, 1)
+    out, lse = c.outputs(512)
+    failing(c, lambda w: dsa.sparse_mla(c.batch, c.q.cuda(), c.cache.cuda(), idx, 64, c.scale, out, lse, w), ws)
+    assert (out[:2] == 0).all() and torch.isneginf(lse[:2]).all() and torch.isfinite(lse[2:]).all()
+    k8, ks = torch.zeros((c.total_keys, 128), dtype=torch.uint8, device="cuda"), torch.ones(c.total_keys, device="cuda")
+    q8, qs = torch.zeros((4, 64, 128), dtype=torch.uint8, device="cuda"), torch.ones((4, 64), device="cuda")
+    scores = torch.full((4, 300), 7.0, device="cuda")
+    failing(c, lambda w: dsa.indexer_scores(c.batch, q8, qs, qs, k8, ks, scores, w), ws)
+    assert (scores[:2] == 7.0).all() and (scores[2, :299] == 0).all() and (scores[3] == 0).all()
+    cache, before = c.cache.cuda(), c.cache.cuda()
+    new = torch.zeros((4, 576), dtype=torch.bfloat16, device="cuda")
+    failing(c, lambda w: dsa.cache_write(c.batch, new[:, :128].contiguous(), new, k8, ks, cache, w), ws)
+    changed = (cache.view(torch.int16) != before.view(torch.int16)).any(1).nonzero().flatten().tolist()
+    assert changed == c.at[1][298:].tolist()
