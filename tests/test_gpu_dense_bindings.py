@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import long_context_sparse_lightning_b200 as dsa
-from tests.dense_ref import check
+from tests.dense_ref import Case, check
 from tests.test_gpu_expanded_mla import Expanded
 
 pytestmark = pytest.mark.gpu
@@ -42,3 +42,35 @@ def test_expanded_steps_in_one_workspace_of_the_largest():
         dsa.expanded_mla(c.batch, c.q.cuda(), c.up.cuda(), c.cache.cuda()[:, 512:], c.scale, out, lse, ws)
         dsa.check_device_error(ws)
         check(out.cpu(), lse.cpu(), c.exact_expanded(), c.rows)
+
+
+def test_two_captured_graphs_share_a_workspace():
+    # one after the other on a stream: nothing in the workspace is kept from one call for the next
+    a, b, x = Case([1, 2], [3000, 500], 16, 64, seed=45), Case([3], [900], 40, 0, seed=46), Expanded([20], [2600], 4, seed=47)
+    n = max(dsa.workspace_size(dsa.OP_DENSE_MLA, c.batch, 0, c.heads) for c in (a, b))
+    n = max(n, dsa.workspace_size(dsa.OP_EXPANDED_MLA, x.batch, 0, 4))
+    ws = torch.zeros(n, dtype=torch.uint8, device="cuda")
+    runs = []
+    for c, dim in ((a, 512), (b, 512), (x, 128)):
+        q, cache, (out, lse) = c.q.cuda(), c.cache.cuda(), c.outputs(dim)
+        if dim == 128:
+            up = c.up.cuda()
+            call = lambda c=c, q=q, up=up, cache=cache, out=out, lse=lse: dsa.expanded_mla(  # noqa: E731
+                c.batch, q, up, cache[:, 512:], c.scale, out, lse, ws)
+        else:
+            call = lambda c=c, q=q, cache=cache, out=out, lse=lse: dsa.dense_mla(  # noqa: E731
+                c.batch, q, cache, c.scale, out, lse, ws)
+        call()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call()
+        # the graph reads q and the caches by address: `call` keeps them (a capture returns freed memory to the device)
+        runs.append((g, c, out, lse, c.exact_expanded() if dim == 128 else c.exact_dense(), call))
+    for i in (0, 1, 2, 1, 0, 2, 2, 0):
+        g, c, out, lse, want, _ = runs[i]
+        out.fill_(7.0)
+        lse.fill_(7.0)
+        g.replay()
+        dsa.check_device_error(ws)
+        check(out.cpu(), lse.cpu(), want, c.rows)
