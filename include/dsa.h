@@ -45,7 +45,9 @@
  *     dsa_workspace_size(op, ...) bytes.  Its first 16 bytes are a device error
  *     word that kernels set when a bounded wait times out or an index is out of
  *     range; zero the workspace once after allocating it, and read (and clear)
- *     the word with dsa_check_device_error.
+ *     the word with dsa_check_device_error.  One workspace serves calls and captured
+ *     graphs that run one after the other; calls that may overlap on the GPU
+ *     need one each.
  *
  * Ragged batches: query row r belongs to sequence b with cu_q[b] <= r < cu_q[b+1];
  * its i-th query (i = r - cu_q[b]) sits at position t = kv_len[b] - q_len[b] + i,
@@ -290,7 +292,9 @@ DSA_API dsa_status_t dsa_sparse_mla_no_alloc(const dsa_batch_t* batch, const voi
  *   out  [total_q, n_heads, 512] bf16     lse [total_q, n_heads] fp32 or NULL
  *   1 <= n_heads <= 128; ws of dsa_workspace_size(DSA_OP_DENSE_MLA, batch, 0,
  *   n_heads) bytes (k_sel is not read).  Two launches (none with total_q = 0);
- *   sequences of any mix of lengths and of 0 or more query tokens each.
+ *   sequences of any mix of lengths and of 0 or more query tokens each.  The work is
+ *   split for the average number of tokens: a few prompts or long chunks among
+ *   many decode tokens are faster as a batch of their own.
  * Arithmetic: bf16 products accumulated in fp32 on the tensor cores, softmax
  * in fp32, probabilities rounded to bf16 for the second product (relative
  * 2^-8 each at most), one rounding to bf16 at the end.
@@ -360,7 +364,8 @@ DSA_API dsa_status_t dsa_expanded_mla(const dsa_batch_t* batch, const void* q, i
  * DSA_ERR_DEVICE_BOUNDS is recorded, and nothing written outside the arrays, for:
  * a negative length or one that needs more than blocks_per_seq pages (the
  * sequence takes no tokens); too few free pages or a negative page id (entry
- * and slots -1); more than max_tokens tokens (cu_q ends at max_tokens).
+ * and slots -1); more than max_tokens tokens (cu_q ends at max_tokens; kv_len, the
+ * table and pages_used count all that were asked for).
  * ws: at least 256 bytes (device error word).  pos and slots may be NULL when
  * max_tokens is 0, free_pages when n_free is 0. */
 DSA_API dsa_status_t dsa_page_tables(int32_t num_seqs, const int32_t* q_len, const int32_t* kv_before,

@@ -12,10 +12,10 @@
 // rows gets half of that), where the transposed form of the one-CTA kernel
 // pays 34 + 48 cycles for the same work (64 x 16K-32K at 128 heads 771 -> 430 us).
 //
-// A tile of 64 keys takes ~1600 cycles where the cache is in L2: 36 x 26 + 8 x 65 of
-// MMAs, whose operands (Q is read again for every tile) and the tile's arrival
-// come to ~1700 cycles of shared-memory bandwidth.  64 x 16K-32K at 128 heads: 430
-// us cold (4.3 TB/s, 1.02 PFLOP/s), ~510 under the power limit (~1.3 GHz).
+// A tile of 64 keys takes ~1600 cycles where the cache is in L2.  Its MMAs take 1456 by their
+// measured rates (36 x 26 + 8 x 65); their operands (Q is read again for every tile) and the
+// tile's arrival are ~212 KB of shared-memory traffic, ~1660 cycles at 128 bytes each.  64 x 16K-32K at
+// 128 heads: 409 us cold (4.5 TB/s, 1.07 PFLOP/s), ~500 under the power limit (~1.3 GHz).
 //
 // A descriptor of a pair names one offset for both CTAs, which ties the two
 // uses of a tile together: block d of a tile's stage holds this CTA's own keys

@@ -18,8 +18,8 @@
 // 16 per cycle, so both units have to be kept busy at once.  Measured: ~3360 cycles
 // a key tile (the products take 1580 a row tile: S reads 128 B/clk of shared
 // memory beside the arriving tiles; handing the probabilities over in two halves
-// changed nothing).  8K at 16 heads 273 us (1.26 PFLOP/s of useful work, 77 % of the burst
-// GEMM rate), 4K at 128 heads 620 us (1.11 PFLOP/s), ~700 under the power limit.
+// changed nothing).  8K at 16 heads 269 us (1.28 PFLOP/s of useful work, 78 % of the burst
+// GEMM rate), 4K at 128 heads 611 us (1.13 PFLOP/s), 700-730 under the power limit.
 //
 // Roles: warp 0 TMA, warp 1 MMAs of both tiles, warps 2-3 clean the value
 // tiles on the border (below), warps 4-7 and 8-11 softmax and epilogue of the tiles.
@@ -43,8 +43,12 @@ constexpr int kKeys = 128;                 // keys per tile
 constexpr int kBlk = 128 * 128;            // one [128 rows x 64 dims] block, 128-byte swizzle
 constexpr int kSlots = 8;                  // ring of key / value blocks, 3 + 2 per tile
 __device__ __forceinline__ int ring(int block) { return block & (kSlots - 1); }
-constexpr int64_t kL2Bytes = 64 << 20;     // of L2 that a group of heads may take
-constexpr int kSplitTiles = 3;             // key tiles a part of a split has at least
+// Of the 126 MB of L2, what a group of heads may take (32, 64, 96 MB, all heads in one group: 4K at 128 heads
+// 669, 665, 662, 687 us; 8K at 16 heads, one head after the other, 1.2 x as long).
+constexpr int64_t kL2Bytes = 64 << 20;
+// Key tiles a part of a split has at least (2, 3, 4, 6: 20 tokens over 3000 keys at 2 heads 13.3, 14.3, 16.2,
+// 18.8 us, 1 over 5000 at 16 heads 19.9, 19.9, 19.9, 22.3).
+constexpr int kSplitTiles = 3;
 constexpr int kThreads = 12 * 32;
 constexpr uint32_t kRegLow = 120, kRegHigh = 192;    // 128 * (120 + 2 * 192) = 384 * 168
 constexpr uint32_t kTmemCols = 512;
@@ -513,7 +517,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c = 0; c < 2; ++c) {
           uint4* blk = reinterpret_cast<uint4*>(sm + OFF_KV + ring(5 * i + 3 + c) * kBlk);
           for (int u = 8 * max(first, dead) + tid - 64; u < kBlk / 16; u += 64) blk[u] = make_uint4(0, 0, 0, 0);
-          // row r of the block is position i * 128 + r; unit u of it holds dims 8 (u ^ (r & 7)) ..
+          // row r of the block is position key0 + r; unit u of it holds dims 8 (u ^ (r & 7)) ..
 #pragma unroll 1
           for (int u0 = 8 * first + tid - 64; u0 < 8 * dead; u0 += 4 * 64) {
             uint4 v[4];
