@@ -84,7 +84,8 @@ struct Aux {
     float mx[2][2][64];                     // per warpgroup and half of a tile's keys: row maxima / row sums
   };
   float ref[64];                            // the rows' references
-  int32_t lost[2];                          // item parity: 1 + number of an item that hidden values were cleaned out of
+  int32_t lost[2];                          // by turns of the items with tiles: number (from 1) of one that hidden
+                                            // values were cleaned out of
 };
 static_assert(sizeof(Aux) <= 2048, "");
 
@@ -525,7 +526,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                        "r"(pk[4 * u]), "r"(pk[4 * u + 1]), "r"(pk[4 * u + 2]), "r"(pk[4 * u + 3])
                        : "memory");
         wait(&ax->v_full[s], (t / kStages) & 1, 584);
-        if (border) clean_values(sm + OFF_KV + s * kStage, pos0, it.lo, min_lim, it.last, &ax->lost[k & 1], k + 1, st);
+        if (border) clean_values(sm + OFF_KV + s * kStage, pos0, it.lo, min_lim, it.last, &ax->lost[n_o & 1], n_o + 1, st);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive_remote(p_full0 + 8 * (t & 1));
@@ -550,8 +551,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         ++n_o;
         tc_fence_after();
       }
-      // read before o_free, which the item after next, whose flag this will be, waits for
-      const bool lost = *static_cast<volatile int32_t*>(&ax->lost[k & 1]) == k + 1;
+      // read before o_free, which the next item's products wait for, and so the one after it, whose flag this will be
+      const bool lost = it.n_tiles > 0 && *static_cast<volatile int32_t*>(&ax->lost[(n_o - 1) & 1]) == n_o;
       float* dst32 = fp32_rows(p, it, kN);
       // 64 dims at a time.  A thread has a row's, which would go out as 32 rows' sectors an
       // instruction; four lanes exchange theirs first, so that each row gets whole lines (16K
@@ -602,15 +603,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0 && !(unit == 0 && n_o - 1 == p.skip_arrival)) mbar_arrive_remote(o_free);
       }
-      if (lost) {
+      // the outputs are written, mx and ref may be rewritten
+      if (bar_any(lost, 1, kSoftThreads)) {
         // this CTA's rows of the item, of all dims
-        bar_sync(1, kSoftThreads);    // the outputs are written
         const int r0 = 64 * static_cast<int>(rank);
         write_nan(p.pt, p.kv, it.b, it.kstart, hidden(it, min_lim), min(it.rows - r0, 64), it.base,
                   it.row0 + r0 - it.seq_row0, H, dst32 == nullptr ? nullptr : dst32 + r0 * 512,
                   p.out + static_cast<int64_t>(it.row0 + r0) * 512, tid - 128, kSoftThreads);
       }
-      bar_sync(1, kSoftThreads);      // mx and ref may be rewritten
     }
   }
   tc_fence_before();

@@ -63,3 +63,31 @@ def test_rows_whose_scores_are_all_minus_infinity(heads, kv):
     assert torch.isnan(out[:2, :, 7].float()).all()
     rest = torch.cat([out[:2, :, :7], out[:2, :, 8:]], -1)
     assert (rest == 0).all()
+
+
+def test_infinite_values_among_many_items_of_a_pair():
+    # items without keys (sequences out of range) among those that the pairs walk, infinities in most others
+    n, heads = 400, 64
+    c = Case([2] * n, [40 + (37 * i) % 300 for i in range(n)], heads, 64, seed=27)
+    clean = c.exact_dense()[0]
+    bad = [i % 5 != 0 and i % 3 == 0 for i in range(n)]          # kv_len out of range
+    for i in range(n):
+        if i % 4 != 3:
+            c.cache[c.at[i][-1], (13 * i) % 512] = INF           # the last token alone sees it
+        if bad[i]:
+            c.kv[i] = 1
+    out, lse = c.dense(check=False)
+    for i in range(n):
+        a, b = out[2 * i].double(), out[2 * i + 1].double()
+        if bad[i]:
+            assert (a == 0).all() and (b == 0).all() and torch.isneginf(lse[2 * i:2 * i + 2]).all()
+            continue
+        assert (a - clean[2 * i]).norm() <= 2.0 ** -8 * clean[2 * i].norm()
+        if i % 4 == 3:
+            assert (b - clean[2 * i + 1]).norm() <= 2.0 ** -8 * clean[2 * i + 1].norm()
+        else:
+            down = c.q[2 * i + 1, :, (13 * i) % 512] < 0         # the score is -inf, or +inf
+            assert torch.isnan(b[~down]).all() and torch.isfinite(lse[2 * i + 1][down]).all()
+            want = torch.zeros((heads, 512), dtype=torch.bool)
+            want[:, (13 * i) % 512] = True
+            assert torch.equal(torch.isnan(b)[down], want[down])
