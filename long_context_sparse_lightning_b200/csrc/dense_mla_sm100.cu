@@ -409,6 +409,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         ld_scores(tmem + lane_base + TM_S + sb * 64, s);
         tmem_ld_wait();
         tc_fence_before();
+        // the first pair's barrier, long complete, shows what the loading warp has noted for the slot
+        wait(&ax->pair_full[4 * t % C::PAIR_SLOTS], (4 * t / C::PAIR_SLOTS) & 1, 534);
         const int skip = ax->skip[4 * t % C::PAIR_SLOTS];   // kept until the slot is refilled, after this tile's product
         __syncwarp();
         if (lane == 0) mbar_arrive(&ax->s_empty[sb]);
